@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(HERE, "libsffn.so")
 # status codes (include/sffn.h)
 SFFN_OK, SFFN_ERR_INVALID_ARG, SFFN_ERR_UNSUPPORTED, SFFN_ERR_ALLOC, SFFN_ERR_CUDA, \
     SFFN_ERR_TIMEOUT, SFFN_ERR_DEVICE, SFFN_ERR_NO_DEVICE = range(8)
-SFFN_BF16, SFFN_FP32 = 0, 1
+SFFN_BF16, SFFN_FP32, SFFN_E4M3 = 0, 1, 2
 SFFN_MODE_RELU_THRESHOLD, SFFN_MODE_WINA_TOPK, SFFN_MODE_WINA_FULL_H = 0, 1, 2
 SFFN_ACT_RELU, SFFN_ACT_SILU = 0, 1
 SFFN_PATH_AUTO, SFFN_PATH_ROWS, SFFN_PATH_TILES = 0, 1, 2
@@ -51,6 +51,20 @@ class sffn_moe_desc(ctypes.Structure):
                 ("A", ctypes.POINTER(ctypes.c_void_p)), ("B", ctypes.POINTER(ctypes.c_void_p)),
                 ("W_up", ctypes.POINTER(ctypes.c_void_p)), ("W_down", ctypes.POINTER(ctypes.c_void_p)),
                 ("gate_bias", ctypes.POINTER(ctypes.c_void_p))]
+
+
+class sffn_rmsnorm_desc(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int), ("x_dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
+                ("y_dtype", ctypes.c_int)]
+
+
+class sffn_qlinear_desc(ctypes.Structure):
+    _fields_ = [("d_in", ctypes.c_int), ("d_out", ctypes.c_int), ("Wq", ctypes.c_void_p), ("Ws", ctypes.c_void_p)]
+
+
+class sffn_grouped_desc(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int), ("d_in", ctypes.c_int), ("d_out", ctypes.c_int), ("W", ctypes.c_void_p)]
 
 
 class sffn_stats(ctypes.Structure):
@@ -148,6 +162,27 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sffn_moe_timing_end.argtypes = [vp, ip, vp, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ip),
                                         ctypes.POINTER(ip)]
     lib.sffn_moe_timing_end.restype = st
+    sz = ctypes.c_size_t
+    lib.sffn_rmsnorm_forward.argtypes = [ctypes.POINTER(sffn_rmsnorm_desc), vp, vp, ip, vp, vp, vp, vp]
+    lib.sffn_rmsnorm_backward.argtypes = [ctypes.POINTER(sffn_rmsnorm_desc), vp, vp, vp, ip, vp, vp, vp, sz, vp]
+    lib.sffn_rmsnorm_workspace_bytes.argtypes = [ip, ip, ctypes.POINTER(sz)]
+    lib.sffn_quantize_rows.argtypes = [vp, ip, ip, ip, vp, vp, vp]
+    lib.sffn_quantize_blocks.argtypes = [vp, ip, ip, ip, vp, vp, vp]
+    lib.sffn_qlinear_create.argtypes = [ctypes.POINTER(sffn_qlinear_desc), vp, ctypes.POINTER(vp)]
+    lib.sffn_qlinear_forward.argtypes = [vp, vp, vp, ip, vp, ip, vp]
+    lib.sffn_qlinear_read_status.argtypes = [vp, vp]
+    lib.sffn_qlinear_destroy.argtypes = [vp]
+    lib.sffn_grouped_create.argtypes = [ctypes.POINTER(sffn_grouped_desc), vp, ctypes.POINTER(vp)]
+    lib.sffn_grouped_forward.argtypes = [vp, vp, vp, ip, vp, ip, vp]
+    lib.sffn_grouped_backward_input.argtypes = [vp, vp, vp, ip, vp, ip, vp]
+    lib.sffn_grouped_backward_weight.argtypes = [vp, vp, vp, vp, ip, vp, ip, vp]
+    lib.sffn_grouped_read_status.argtypes = [vp, vp]
+    lib.sffn_grouped_destroy.argtypes = [vp]
+    for fn in ("rmsnorm_forward", "rmsnorm_backward", "rmsnorm_workspace_bytes", "quantize_rows", "quantize_blocks",
+               "qlinear_create", "qlinear_forward", "qlinear_read_status", "qlinear_destroy", "grouped_create",
+               "grouped_forward", "grouped_backward_input", "grouped_backward_weight", "grouped_read_status",
+               "grouped_destroy"):
+        getattr(lib, "sffn_" + fn).restype = st
     lib.sffn_version.argtypes = []
     lib.sffn_version.restype = ctypes.c_char_p
     _lib = lib

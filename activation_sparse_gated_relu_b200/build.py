@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -15,11 +16,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsffn.so")
 HEADER = os.path.join(ROOT, "include", "sffn.h")
 
-NVCC_FLAGS = [
-    "-std=c++17", "-O3", "-lineinfo",
-    "-gencode", "arch=compute_100a,code=sm_100a",
-    "-Xcompiler", "-fPIC", "-shared",
-]
+ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC"]
+UNITS = ["sffn.cu", "layer.cu"]   # translation units, compiled side by side
 
 
 def _nvcc() -> str:
@@ -45,16 +44,35 @@ def up_to_date() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/sffn.cu into libsffn.so next to this file; return its path."""
+    """Compile csrc/ into libsffn.so next to this file; return its path."""
     if not force and up_to_date():
         return LIB
-    tmp = LIB + ".tmp"
-    cmd = [_nvcc(), *NVCC_FLAGS, "-o", tmp, os.path.join(CSRC, "sffn.cu")]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+    nvcc = _nvcc()
+    with tempfile.TemporaryDirectory() as tmp_dir:
+        objects, running = [], []
+        for unit in UNITS:
+            obj = os.path.join(tmp_dir, unit + ".o")
+            cmd = [nvcc, *NVCC_FLAGS, "-c", "-o", obj, os.path.join(CSRC, unit)]
+            if verbose:
+                print(" ".join(cmd), file=sys.stderr)
+            log = open(obj + ".log", "w+")
+            running.append((subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT), log))
+            objects.append(obj)
+        failed = []
+        for proc, log in running:
+            if proc.wait() != 0:
+                log.seek(0)
+                failed.append(log.read())
+            log.close()
+        if failed:
+            raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+        tmp = LIB + ".tmp"
+        cmd = [nvcc, *ARCH, "-Xcompiler", "-fPIC", "-shared", "-o", tmp, *objects]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
     os.replace(tmp, LIB)
     return LIB
 

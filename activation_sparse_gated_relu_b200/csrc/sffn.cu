@@ -29,6 +29,7 @@
 #include <vector>
 
 #include "../../include/sffn.h"
+#include "host_util.cuh"
 #include "epilogues.cuh"
 #include "decode_fused.cuh"
 #include "tc_gate_persist.cuh"
@@ -60,24 +61,6 @@ const char* const kLabelNames[L_COUNT] = {"gate_lowrank_z", "gate", "wina_topk",
                                           "bwd_index", "bwd_token", "bwd_neuron", "bwd_dense", "tile_fused"};
 constexpr int kMaxTokensLimit = 16384;
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
-
 // 2-D bf16 tensor map over a row-major [rows][inner] matrix, box = 64 x box_rows,
 // 128-byte swizzle (the K-major operand layout of the tile kernel).
 bool make_map(CUtensorMap* m, const void* base, long long inner, long long rows, int box_rows) {
@@ -94,7 +77,6 @@ bool make_map(CUtensorMap* m, const void* base, long long inner, long long rows,
 }
 
 int pick_bn(int n) { return n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256; }
-int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // K splits of the z = x·A GEMM: only with one token tile (up to 256 tokens),
 // at most Z_MAX_SPLITS, at least 4 K blocks each, and no more CTAs than SMs
@@ -260,37 +242,6 @@ TfSchedule tf_schedule(int n_chunks, int kd, int kg, int P, int Rt, int Md, int 
   return S;
 }
 
-// Launch with programmatic dependent launch: the kernel may be scheduled while
-// the previous kernel on the stream drains; it calls griddepcontrol.wait before
-// touching data an earlier kernel writes or reads.  cluster_x > 1 also sets
-// the thread-block cluster size.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       int cluster_x, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  int n = 0;
-  at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[n].val.programmaticStreamSerializationAllowed = 1;
-  ++n;
-  if (cluster_x > 1) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n].val.clusterDim.x = cluster_x;
-    at[n].val.clusterDim.y = 1;
-    at[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  cfg.attrs = at;
-  cfg.numAttrs = n;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-  if (e != cudaSuccess) cudaGetLastError();
-  return e;
-}
-
 template <int BN, class Epi>
 cudaError_t launch_tc_bn(dim3 grid, cudaStream_t st, const CUtensorMap& a0, const CUtensorMap& b0,
                          const CUtensorMap& a1, const CUtensorMap& b1, const TcArgs& args,
@@ -346,7 +297,6 @@ cudaError_t set_tc_attrs() {
   return e;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 
@@ -505,17 +455,6 @@ struct Arena {
   }
 };
 
-template <typename T>
-bool dalloc(T** p, size_t bytes) {
-  if (bytes == 0) bytes = 16;
-  void* q = nullptr;
-  if (cudaMalloc(&q, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  *p = static_cast<T*>(q);
-  return true;
-}
 
 void tmark(KTiming* h, cudaStream_t st, int label) {
   if (!h->tm_on || h->tm_cur < 0) return;

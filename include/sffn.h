@@ -75,7 +75,9 @@ typedef enum {
   SFFN_ERR_NO_DEVICE = 7      /* no usable sm_100 device                           */
 } sffn_status;
 
-typedef enum { SFFN_BF16 = 0, SFFN_FP32 = 1 } sffn_dtype;
+/* SFFN_E4M3 (8-bit codes with fp32 scales) is a type of the operators around
+ * the FFN only (sffn_rmsnorm_*, sffn_qlinear_*). */
+typedef enum { SFFN_BF16 = 0, SFFN_FP32 = 1, SFFN_E4M3 = 2 } sffn_dtype;
 /* Selection of the kept neurons.
  *   RELU_THRESHOLD: keep iff |sigma(g)| > threshold;
  *   WINA_TOPK     : per token the k largest |sigma(g_j)|·||W_down[j,:]||_2 (WINA
@@ -476,6 +478,124 @@ sffn_status sffn_moe_read_status(sffn_moe_handle* h, void* cuda_stream);
 sffn_status sffn_moe_timing_begin(sffn_moe_handle* h, int max_forwards, int stride);
 sffn_status sffn_moe_timing_end(sffn_moe_handle* h, int max_kernels, char (*names)[32], float* total_ms,
                                 int* launches, int* n_kernels);
+
+/* ------------------------------------------------------------------------
+ * Operators around the sparse FFN: the norm that feeds it, a linear layer in
+ * 8 bits, and dense experts' products.  General rules: all tensors are
+ * row-major DEVICE memory on 16-byte boundaries, on the calling thread's
+ * current device; calls are asynchronous on cuda_stream, allocate nothing and
+ * may be captured into a CUDA graph; a handle's calls keep no state between
+ * one another (its status word only collects errors), so calls of one handle
+ * may overlap on several streams.  Row counts go up to 2^24.
+ *
+ * 8-bit values: e4m3 codes with one fp32 scale per group, value = code·scale.
+ * For a group of largest magnitude m = max(|v|, 1e-30): scale = m / 448 and
+ * code = e4m3(v · (448 / m)), to nearest, ties to even.  A NaN stays in its own
+ * element; a group that holds an infinity has no finite values.
+ * ------------------------------------------------------------------------ */
+
+/* RMS norm with the residual's addition, over rows of d columns:
+ *
+ *     s = residual + x      (s = x without a residual)
+ *     y = s · rstd · weight,   rstd = 1 / sqrt(mean(s^2) + eps)
+ *
+ * y uses the unrounded fp32 sum.  x [T][d] bf16 or fp32 (sffn_forward's out is
+ * fp32); residual [T][d] bf16 or fp32 or NULL; residual_out [T][d] receives s
+ * in the residual's type and may be the residual itself (NULL iff residual is
+ * NULL); weight [d] bf16 or fp32; y [T][d] bf16, fp32, or e4m3 codes with
+ * scale [T][ceil(d/128)], one for each 128 columns (scale is NULL for the other
+ * types).  eps finite, >= 0.
+ * Limits: d % 8 == 0, d <= 16384 (SFFN_ERR_UNSUPPORTED). */
+typedef struct sffn_rmsnorm_desc {
+  int d;
+  float eps;
+  const void* weight;
+  sffn_dtype weight_dtype;
+  sffn_dtype x_dtype;
+  sffn_dtype residual_dtype;   /* residual and residual_out; the backward's s, ds and dx */
+  sffn_dtype y_dtype;          /* y; the backward's dy (bf16 or fp32) */
+} sffn_rmsnorm_desc;
+
+sffn_status sffn_rmsnorm_forward(const sffn_rmsnorm_desc* desc, const void* x, const void* residual, int T,
+                                 void* residual_out, void* y, float* scale, void* cuda_stream);
+
+/* Gradients for upstream dy [T][d], given s [T][d] (residual_out, or x without
+ * a residual) and, if not NULL, ds [T][d], the gradient that reaches s past
+ * the norm.  With g = dy·weight and a = sum_j g_j s_j:
+ *     dx = rstd·g - s·a·rstd^3/d + ds   (the gradient of x and of the residual)
+ *     dweight = sum over rows of dy·s·rstd,  fp32 [d], fully overwritten.
+ * dx may be ds, or dy or s where their types agree.  The workspace (device, 16-byte
+ * aligned) holds partial sums of dweight; sums run in a fixed order.  T == 0
+ * writes dweight = 0. */
+sffn_status sffn_rmsnorm_backward(const sffn_rmsnorm_desc* desc, const void* dy, const void* s, const void* ds,
+                                  int T, void* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                                  void* cuda_stream);
+/* Workspace of sffn_rmsnorm_backward for T rows (host only). */
+sffn_status sffn_rmsnorm_workspace_bytes(int d, int T, size_t* bytes);
+
+/* 8-bit codes of rows: x [T][d] bf16 or fp32 -> codes [T][d], scale
+ * [T][ceil(d/128)], one for each 128 columns.  d % 8 == 0. */
+sffn_status sffn_quantize_rows(const void* x, sffn_dtype x_dtype, int T, int d, void* codes, float* scale,
+                               void* cuda_stream);
+/* 8-bit codes of a weight: W [n][k] bf16 or fp32 -> codes [n][k], scale
+ * [ceil(n/128)][ceil(k/128)], one for each block of 128 x 128.  k % 8 == 0. */
+sffn_status sffn_quantize_blocks(const void* W, sffn_dtype w_dtype, int n, int k, void* codes, float* scale,
+                                 void* cuda_stream);
+
+/* Linear layer with both operands in 8 bits (inference):
+ *     y[t][n] = sum_b xs[t][b]·Ws[n/128][b]·sum_{k in block b} xq[t][k]·Wq[n][k],
+ * b over the 128-wide blocks of d_in (the last may be short), blocks scaled
+ * and added in fp32.  Wq [d_out][d_in] and xq [T][d_in] are e4m3 codes, Ws
+ * [ceil(d_out/128)][ceil(d_in/128)] and xs [T][ceil(d_in/128)] their scales.
+ * Limits: d_in % 16 == 0, d_out % 8 == 0, both <= 2^20.  Wq and Ws are
+ * borrowed for the handle's life. */
+typedef struct sffn_qlinear_desc {
+  int d_in, d_out;
+  const void* Wq;
+  const float* Ws;
+} sffn_qlinear_desc;
+
+typedef struct sffn_qlinear_handle sffn_qlinear_handle;
+
+sffn_status sffn_qlinear_create(const sffn_qlinear_desc* desc, void* cuda_stream, sffn_qlinear_handle** out);
+/* y [T][d_out] bf16 or fp32, fully overwritten; T == 0 launches nothing. */
+sffn_status sffn_qlinear_forward(sffn_qlinear_handle* h, const void* xq, const float* xs, int T, void* y,
+                                 sffn_dtype y_dtype, void* cuda_stream);
+sffn_status sffn_qlinear_read_status(sffn_qlinear_handle* h, void* cuda_stream);   /* as sffn_read_status */
+sffn_status sffn_qlinear_destroy(sffn_qlinear_handle* h);
+
+/* Products grouped by expert: rows sorted by expert, offsets [n_experts + 1]
+ * int32 on the DEVICE, expert e owning rows offsets[e] <= r < offsets[e+1]
+ * (groups may be empty).  W [n_experts][d_out][d_in] bf16, borrowed; its
+ * values may change between calls.
+ *     forward          y[r]  = W[e] x[r]                 bf16 or fp32
+ *     backward_input   dx[r] = W[e]^T dy[r]              bf16 or fp32
+ *     backward_weight  dW[e] = sum_{r in e} dy[r] x[r]^T  bf16 or fp32
+ * x [R][d_in], dy [R][d_out] bf16; sums fp32, rounded once.  Rows outside
+ * every group are left as they were in y and dx; dW of an empty group is 0.
+ * A row depends on no other row's values, not even NaN.  Offsets must not
+ * decrease and lie in 0..R: the kernels clamp what does not and record
+ * SFFN_ERR_DEVICE (sffn_grouped_read_status); the results of the groups
+ * concerned are then undefined.
+ * Limits: n_experts <= 1024, d_in % 8 == 0, d_out % 8 == 0, both <= 2^20. */
+#define SFFN_GROUPED_MAX_EXPERTS 1024
+typedef struct sffn_grouped_desc {
+  int n_experts, d_in, d_out;
+  const void* W;
+} sffn_grouped_desc;
+
+typedef struct sffn_grouped_handle sffn_grouped_handle;
+
+sffn_status sffn_grouped_create(const sffn_grouped_desc* desc, void* cuda_stream, sffn_grouped_handle** out);
+sffn_status sffn_grouped_forward(sffn_grouped_handle* h, const void* x, const int32_t* offsets, int R, void* y,
+                                 sffn_dtype y_dtype, void* cuda_stream);
+sffn_status sffn_grouped_backward_input(sffn_grouped_handle* h, const void* dy, const int32_t* offsets, int R,
+                                        void* dx, sffn_dtype dx_dtype, void* cuda_stream);
+sffn_status sffn_grouped_backward_weight(sffn_grouped_handle* h, const void* x, const void* dy,
+                                         const int32_t* offsets, int R, void* dW, sffn_dtype dw_dtype,
+                                         void* cuda_stream);
+sffn_status sffn_grouped_read_status(sffn_grouped_handle* h, void* cuda_stream);   /* as sffn_read_status */
+sffn_status sffn_grouped_destroy(sffn_grouped_handle* h);
 
 /* Library version string. */
 const char* sffn_version(void);

@@ -1,0 +1,207 @@
+"""The experts' grouped products, forward and both gradients, against plain
+products in 64 bits.
+
+Bounds.  Sums over K terms are fp32: off by less than (K + 64) U · sum |a||b|
+whatever their order, plus half a step of the output's type.  On small whole
+numbers, whose sums fp32 holds exactly, the outputs have to be the exact
+values, rounded once."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from activation_sparse_gated_relu_b200 import SFFN_ERR_DEVICE, SFFN_OK, GroupedLinear
+from layer_util import HALF, U, ints, randn, within
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def layout(counts, lead=0):
+    off = [lead]
+    for c in counts:
+        off.append(off[-1] + c)
+    return off, torch.tensor(off, dtype=torch.int32, device="cuda")
+
+
+# counts per expert, rows before the first and behind the last group, d_in, d_out
+CASES = [
+    ([1], 0, 0, 8, 8),
+    ([0], 0, 3, 64, 64),
+    ([5, 0, 3], 0, 0, 64, 128),
+    ([1, 1, 1, 1], 0, 4, 72, 136),
+    ([16, 17, 0, 15], 2, 5, 128, 264),
+    ([33, 0, 0, 64, 1], 0, 0, 200, 256),
+    ([130, 7], 1, 0, 512, 384),
+    ([127, 128, 129], 0, 9, 136, 136),
+    ([255, 0, 257], 3, 1, 320, 520),
+    ([600], 0, 0, 264, 1032),
+    ([0, 0, 300, 0], 0, 20, 1024, 128),
+    ([2] * 40 + [0] * 24, 0, 0, 256, 256),
+    ([70, 3, 0, 900, 1], 7, 11, 648, 776),
+]
+
+
+@pytest.mark.parametrize("counts,lead,tail,k,n", CASES)
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_forward_and_gradients(counts, lead, tail, k, n, out):
+    E, t = len(counts), BF if out == "bf16" else F32
+    off, offsets = layout(counts, lead)
+    R = off[-1] + tail
+    x, dy, W = randn(1, R, k, dtype=BF), randn(2, R, n, dtype=BF), randn(3, E, n, k, dtype=BF, scale=k ** -0.5)
+    op = GroupedLinear(W)
+    y = torch.full((R, n), 7.0, dtype=t, device="cuda")
+    dx = torch.full((R, k), 7.0, dtype=t, device="cuda")
+    dW = torch.full((E, n, k), float("nan"), dtype=t, device="cuda")
+    op.forward(x, offsets, out=out, y=y)
+    op.backward(x, dy, offsets, out=out, dx=dx, dW=dW)
+    torch.cuda.synchronize()
+    assert op.read_status() == SFFN_OK
+    for rows in (slice(0, lead), slice(off[-1], R)):
+        assert (y[rows] == 7).all() and (dx[rows] == 7).all()
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        xe, de, we = x[r].double(), dy[r].double(), W[e].double()
+        for got, a, b, K in ((y[r], xe, we.t(), k), (dx[r], de, we, n), (dW[e], de.t(), xe, counts[e])):
+            ref = a @ b
+            within(got, ref, ref.abs() * HALF[t] + (K + 64) * U * (a.abs() @ b.abs()) + 1e-38, f"expert {e}")
+
+
+@pytest.mark.parametrize("counts,lead,tail,k,n", CASES)
+def test_exact_sums(counts, lead, tail, k, n):
+    # values in -4..4: sums below 16 · 1032 < 2^24 in magnitude
+    E = len(counts)
+    off, offsets = layout(counts, lead)
+    R = off[-1] + tail
+    x, dy, W = ints(4, R, k), ints(5, R, n), ints(6, E, n, k)
+    op = GroupedLinear(W)
+    y = op.forward(x, offsets, out="fp32")
+    g = op.backward(x, dy, offsets, out="fp32")
+    yb = op.forward(x, offsets)
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        ref = (x[r].double() @ W[e].double().t()).float()
+        assert torch.equal(y[r], ref) and torch.equal(yb[r], ref.to(BF))
+        assert torch.equal(g["dx"][r], (dy[r].double() @ W[e].double()).float())
+        assert torch.equal(g["dW"][e], (dy[r].double().t() @ x[r].double()).float())
+    assert op.read_status() == SFFN_OK
+
+
+def test_values_outside_a_group_never_reach_it():
+    # rows of other experts, rows in no group and the weights of other experts hold NaN and infinities
+    counts, k, n = [20, 0, 150, 3], 136, 264
+    off, offsets = layout(counts, 5)
+    R = off[-1] + 6
+    x, dy, W = ints(7, R, k), ints(8, R, n), ints(9, 4, n, k)
+    good = GroupedLinear(W)
+    y, g = good(x, offsets), good.backward(x, dy, offsets)
+    for e in (0, 2, 3):
+        bx, bd, bw = x.clone(), dy.clone(), W.clone()
+        mine = slice(off[e], off[e + 1])
+        other = torch.ones(R, dtype=torch.bool, device="cuda")
+        other[mine] = False
+        bx[other], bd[other] = float("nan"), float("inf")
+        for f in range(4):
+            if f != e:
+                bw[f] = float("inf")
+        op = GroupedLinear(bw)
+        y2, g2 = op(bx, offsets), op.backward(bx, bd, offsets)
+        assert torch.equal(y2[mine], y[mine])
+        assert torch.equal(g2["dx"][mine], g["dx"][mine])
+        assert torch.equal(g2["dW"][e], g["dW"][e])
+        assert (g2["dW"][1] == 0).all()
+
+
+def test_offsets_out_of_range_are_reported_and_clamped():
+    op = GroupedLinear(ints(10, 3, 64, 64))
+    x, dy = ints(11, 40, 64), ints(12, 40, 64)
+    good = torch.tensor([0, 10, 20, 40], dtype=torch.int32, device="cuda")
+    for bad in ([0, 10, 20, 41], [-5, 10, 20, 40], [0, 30, 20, 40], [0, 2 ** 31 - 1, 20, 40], [-2 ** 31, 5, 5, 2 ** 30]):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        for call in (lambda: op.forward(x, off), lambda: op.backward(x, dy, off)):
+            call()
+            assert op.read_status() == SFFN_ERR_DEVICE
+            assert op.read_status() == SFFN_OK
+    op.forward(x, good), op.backward(x, dy, good)
+    assert op.read_status() == SFFN_OK
+
+
+def test_no_rows_and_many_experts():
+    op = GroupedLinear(ints(13, 1024, 16, 16))
+    off = torch.zeros(1025, dtype=torch.int32, device="cuda")
+    x = torch.empty(0, 16, dtype=BF, device="cuda")
+    assert op(x, off).shape == (0, 16)
+    g = op.backward(x, x, off)
+    assert g["dx"].shape == (0, 16) and (g["dW"] == 0).all()
+    counts = [(i * 7) % 3 for i in range(1024)]
+    o, offsets = layout(counts)
+    x = ints(14, o[-1], 16)
+    y = op(x, offsets, out="fp32")
+    e = torch.repeat_interleave(torch.arange(1024), torch.tensor(counts)).cuda()
+    assert torch.equal(y, torch.einsum("rk,rnk->rn", x.double(), op.W[e].double()).float())
+    g = op.backward(x, x, offsets)
+    dW = torch.zeros(1024, 16, 16, dtype=torch.float64, device="cuda")
+    dW.index_add_(0, e, torch.einsum("rn,rk->rnk", x.double(), x.double()))
+    assert torch.equal(g["dW"], dW.float())
+
+
+def test_weights_may_change_between_calls():
+    W = ints(15, 2, 128, 64)
+    op = GroupedLinear(W)
+    off, offsets = layout([9, 4])
+    x = ints(16, 13, 64)
+    op(x, offsets)
+    W.copy_(ints(17, 2, 128, 64))
+    assert torch.equal(op(x, offsets, out="fp32")[9:], (x[9:].double() @ W[1].double().t()).float())
+
+
+def test_graph_replay_with_new_offsets_and_overlapping_calls():
+    E, k, n, R = 4, 256, 512, 300
+    W, x, dy = ints(18, E, n, k), ints(19, R, k), ints(20, R, n)
+    op = GroupedLinear(W)
+    _, a = layout([100, 0, 150, 50])
+    _, b = layout([3, 250, 0, 47])
+    off = a.clone()
+    torch.cuda.synchronize()
+    op(x, off), op.backward(x, dy, off)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        y = op(x, off)
+        grad = op.backward(x, dy, off)
+    for o in (b, a):
+        off.copy_(o)
+        g.replay()
+        torch.cuda.synchronize()
+        want = op.backward(x, dy, o)
+        assert torch.equal(y, op(x, o)) and torch.equal(grad["dx"], want["dx"]) and torch.equal(grad["dW"], want["dW"])
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [op.backward(x, dy, a, stream=(s, t)[i & 1].cuda_stream) for i in range(12)]
+    torch.cuda.synchronize()
+    want = op.backward(x, dy, a)
+    assert all(torch.equal(v["dx"], want["dx"]) and torch.equal(v["dW"], want["dW"]) for v in outs)
+    assert op.read_status() == SFFN_OK
+
+
+def test_gradients_against_differences():
+    # the 64-bit formulas against differences of L = sum(y·dy), y = W[e(r)] x[r] (linear: any step is exact to rounding)
+    counts, k, n = [3, 0, 2], 8, 16
+    off, _ = layout(counts)
+    x, dy, W = randn(21, 5, k).double(), randn(22, 5, n).double(), randn(23, 3, n, k).double()
+    e = torch.tensor([0, 0, 0, 2, 2], device="cuda")
+
+    def loss(x, W):
+        return (torch.einsum("rk,rnk->rn", x, W[e]) * dy).sum()
+
+    dx = torch.einsum("rn,rnk->rk", dy, W[e])
+    dW = torch.stack([dy[off[i]:off[i + 1]].t() @ x[off[i]:off[i + 1]] for i in range(3)])
+    for r, c in ((0, 0), (3, 7)):
+        h = torch.zeros_like(x)
+        h[r, c] = 0.5
+        assert abs(loss(x + h, W) - loss(x - h, W) - dx[r, c]) < 1e-12
+    for i, o, c in ((0, 3, 2), (1, 0, 0), (2, 15, 7)):
+        h = torch.zeros_like(W)
+        h[i, o, c] = 0.5
+        assert abs(loss(x, W + h) - loss(x, W - h) - dW[i, o, c]) < 1e-12
