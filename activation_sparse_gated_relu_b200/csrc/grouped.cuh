@@ -5,12 +5,61 @@
 //   input     dx[r] = W[e]^T dy[r]
 //   weight    dW[e] = sum_{r in e} dy[r] x[r]^T
 //
-// bf16 operands, fp32 sums.
+// bf16 operands, fp32 sums.  All three are one tile kernel, D[m][c] = sum_k
+// A[m][k] B[c][k] on the tensor cores, with the weight side as the MMA's rows m
+// (128 TMEM lanes per CTA) and the ragged side as its columns c:
+//
+//             m          c               k               A            B
+//   forward   n          e's rows        k               W, K-major   x, K-major
+//   input     k          e's rows        n               W, M-major   dy, K-major
+//   weight    k          n               e's rows        x, M-major   dy, N-major
+//
+// so that a group costs columns rounded up to 16 or 32, not to 128 rows, and
+// an M- or N-major operand is read as it lies, without a transposed copy.  D's
+// column c is a row of the output and its lanes are consecutive there, so
+// every store of a warp is one run of 32 values.
+//
+// Persistent CTAs (or CTA pairs: 256 rows, each CTA holding half of the
+// columns' operand) walk the tiles of all experts; two accumulators in TMEM
+// let the MMAs of a tile run beside the stores of the tile before.
 #pragma once
 
+#include "ptx_pair.cuh"
 #include "vec8.cuh"
 
 namespace sffn {
+
+enum { GROUPED_FWD = 0, GROUPED_DX = 1, GROUPED_DW = 2 };
+constexpr int GROUPED_MAX_E = 1024;
+constexpr int GT_EPI_WARPS = 8;                        // two warpgroups, every other 32 columns each
+constexpr int GT_PRODUCER = GT_EPI_WARPS, GT_MMA = GT_EPI_WARPS + 1;
+constexpr int GT_THREADS = (GT_EPI_WARPS + 2) * 32;
+constexpr int GT_BK = 64;                              // bf16 values of k per stage
+constexpr int GT_SMEM = 227 * 1024;
+
+// BN: columns per tile.
+template <int CTAS, int BN>
+struct GtCfg {
+  static constexpr int B_ROWS = BN / CTAS;             // columns whose operand a CTA holds
+  static constexpr int A_BYTES = 128 * GT_BK * 2;
+  static constexpr int B_BYTES = B_ROWS * GT_BK * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int TABLE = (3 * (GROUPED_MAX_E + 1) * 4 + 127) & ~127;
+  static constexpr int FIXED = 1024 /*align*/ + 256 /*barriers*/ + TABLE;
+  static constexpr int RAW = (GT_SMEM - FIXED) / STAGE;
+  static constexpr int STAGES = RAW > 10 ? 10 : RAW;
+  static constexpr int SMEM = FIXED + STAGES * STAGE;
+};
+
+struct GroupedArgs {
+  const int* off;       // [E + 1]
+  void* out;
+  int E, R;
+  int M, N, K;          // rows m; columns c (weight gradient); inner size k (forward and input gradient)
+  int out_f32;
+  int kchunk;           // k blocks that the tensor core adds up before they join the fp32 sum in registers
+  uint32_t* status;
+};
 
 // Group e's rows [a, b), clamped to [0, R]; false if the offsets are out of
 // range or run backwards (the group is then what the clamping leaves).
@@ -21,51 +70,326 @@ __device__ __forceinline__ bool group_rows(const int* off, int e, int R, int* a,
   return u >= 0 && v >= u && v <= R;
 }
 
-struct GroupedArgs {
-  const __nv_bfloat16* a;   // x or dy
-  const __nv_bfloat16* b;   // W, or (weight gradient) x
-  const int* off;           // [E + 1]
-  void* out;
-  int E, R, k, n, out_f32;
-  uint32_t* status;
+// The tiles of all experts in order, one role's walk over them.
+template <int MODE, int CTAS, int BN>
+struct GtWalk {
+  const int *ra, *rb, *first;   // group rows, first tile of each expert ([E] the total)
+  int M, N, K, e;
+  // the current tile
+  int m0;                       // first row m of the tile (of the pair)
+  int c0, cols, bn;             // first column, columns stored, columns computed
+  int krow;                     // weight gradient: first row of the group
+  int kbs, ktail;               // k blocks, and values in the last one
+  size_t orow;                  // output row of column 0
+
+  __device__ __forceinline__ void set(int w) {
+    while (w >= first[e + 1]) ++e;
+    const int t = w - first[e], a = ra[e], rows = rb[e] - a;
+    constexpr int STEP = 16 * CTAS;
+    if (MODE == GROUPED_DW) {
+      const int nt = (N + BN - 1) / BN;
+      m0 = t / nt * (128 * CTAS);
+      c0 = t % nt * BN;
+      cols = min(BN, N - c0);
+      krow = a;
+      kbs = (rows + GT_BK - 1) / GT_BK;
+      ktail = rows - (kbs - 1) * GT_BK;
+      orow = (size_t)e * N + c0;
+    } else {
+      // the fewest tiles of at most BN columns, even ones
+      const int nt = (rows + BN - 1) / BN;
+      const int each = ((rows + nt - 1) / nt + STEP - 1) / STEP * STEP;
+      m0 = t / nt * (128 * CTAS);
+      c0 = a + t % nt * each;
+      cols = min(each, a + rows - c0);
+      kbs = (K + GT_BK - 1) / GT_BK;
+      ktail = K - (kbs - 1) * GT_BK;
+      orow = (size_t)c0;
+    }
+    bn = (cols + STEP - 1) / STEP * STEP;
+  }
 };
 
-__device__ __forceinline__ void put(void* out, int f32, size_t at, float v) {
-  if (f32) reinterpret_cast<float*>(out)[at] = v;
-  else reinterpret_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16(v);
-}
+template <int MODE, int CTAS, int BN>
+__global__ void __launch_bounds__(GT_THREADS, 1)
+k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
+          const __grid_constant__ CUtensorMap mB32, const GroupedArgs args) {
+  using Cfg = GtCfg<CTAS, BN>;
+  using Walk = GtWalk<MODE, CTAS, BN>;
+  constexpr int STAGES = Cfg::STAGES;
+  constexpr uint32_t NCOLS = BN <= 16 ? 32 : 2 * BN;     // two accumulators, a power of two of at least 32
+  constexpr bool A_MN = MODE != GROUPED_FWD, B_MN = MODE == GROUPED_DW;
+  static_assert(NCOLS <= 512 && (NCOLS & (NCOLS - 1)) == 0, "TMEM columns");
+  static_assert(!B_MN || Cfg::B_ROWS % 64 == 0, "N-major columns come in boxes of 64");
 
-// MODE 0: y; 1: dx.  One CTA row per expert (blockIdx.y), grid-stride over its rows.
-template <int MODE>
-__global__ void __launch_bounds__(256) k_grouped_rows(const GroupedArgs a) {
-  griddep_wait();
-  const int e = blockIdx.y;
-  int r0, r1;
-  if (!group_rows(a.off, e, a.R, &r0, &r1) && threadIdx.x == 0) atomicOr(a.status, DEV_ERR_RANGE);
-  const int cols = MODE == 0 ? a.n : a.k, inner = MODE == 0 ? a.k : a.n;
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31);
-  if (c >= cols) return;
-  const __nv_bfloat16* W = a.b + (size_t)e * a.n * a.k;
-  for (int r = r0 + (threadIdx.x >> 5); r < r1; r += 8) {
-    float acc = 0.0f;
-    for (int i = 0; i < inner; ++i)
-      acc += __bfloat162float(a.a[(size_t)r * inner + i]) *
-             __bfloat162float(MODE == 0 ? W[(size_t)c * a.k + i] : W[(size_t)i * a.k + c]);
-    put(a.out, a.out_f32, (size_t)r * cols + c, acc);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * Cfg::STAGE);
+  uint64_t* empty = full + STAGES;
+  uint64_t* accfull = empty + STAGES;   // [2]
+  uint64_t* accfree = accfull + 2;      // [2]
+  uint64_t* tailbar = accfree + 2;
+  uint64_t* mma_done = tailbar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 * STAGES + 6) * 8 + 8 <= 256, "barrier area");
+  int* ra = reinterpret_cast<int*>(smem + STAGES * Cfg::STAGE + 256);
+  int* rb = ra + GROUPED_MAX_E + 1;
+  int* first = rb + GROUPED_MAX_E + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
+  const int n_walk = gridDim.x / CTAS, walk0 = blockIdx.x / CTAS;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], CTAS);        // one arrival per CTA's producer
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accfree[b], GT_EPI_WARPS * CTAS);
+    }
+    mbar_init(tailbar, 1);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
   }
-}
+  if (warp == GT_MMA) pair_tmem_alloc<CTAS>(tmem_slot, NCOLS);
+  if (warp == GT_PRODUCER && lane == 0) {
+    tma_prefetch_desc(&mA);
+    tma_prefetch_desc(&mB);
+    if (MODE != GROUPED_DW) tma_prefetch_desc(&mB32);
+  }
+  griddep_wait();   // offsets, operands and outputs belong to the stream order
+  for (int e = threadIdx.x; e < args.E; e += GT_THREADS) {
+    if (!group_rows(args.off, e, args.R, &ra[e], &rb[e]) && blockIdx.x == 0) atomicOr(args.status, DEV_ERR_RANGE);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {   // first tile of each expert: a running sum over experts, 32 at a time
+    const int mt = (args.M + 128 * CTAS - 1) / (128 * CTAS);
+    int base = 0;
+    for (int e0 = 0; e0 < args.E; e0 += 32) {
+      const int e = e0 + lane;
+      int n = 0;
+      if (e < args.E) n = mt * (MODE == GROUPED_DW ? (args.N + BN - 1) / BN : (rb[e] - ra[e] + BN - 1) / BN);
+      int s = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += u;
+      }
+      if (e < args.E) first[e] = base + s - n;
+      base += __shfl_sync(0xFFFFFFFFu, s, 31);
+    }
+    if (lane == 0) first[args.E] = base;
+  }
+  if (CTAS == 2) cluster_sync();   // the barriers of both CTAs are ready
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int n_tiles = first[args.E];
+  Walk t;
+  t.ra = ra;
+  t.rb = rb;
+  t.first = first;
+  t.M = args.M;
+  t.N = args.N;
+  t.K = args.K;
+  t.e = 0;
 
-__global__ void __launch_bounds__(256) k_grouped_weight(const GroupedArgs a) {
-  griddep_wait();
-  const int e = blockIdx.z;
-  int r0, r1;
-  if (!group_rows(a.off, e, a.R, &r0, &r1) && threadIdx.x == 0) atomicOr(a.status, DEV_ERR_RANGE);
-  const int i = blockIdx.x * 32 + (threadIdx.x & 31), o = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (i >= a.k || o >= a.n) return;
-  float acc = 0.0f;
-  for (int r = r0; r < r1; ++r)
-    acc += __bfloat162float(a.a[(size_t)r * a.n + o]) * __bfloat162float(a.b[(size_t)r * a.k + i]);
-  put(a.out, a.out_f32, ((size_t)e * a.n + o) * a.k + i, acc);
+  if (warp == GT_PRODUCER) {
+    // --------------------------------------------------------- TMA producer
+    // The whole warp walks along, so that its lanes can clear the rows behind
+    // a group's end.
+    int it = 0, tails = 0;
+    bool ok = true;
+    for (int w = walk0; w < n_tiles && ok; w += n_walk) {
+      t.set(w);
+      const int half = t.bn / CTAS, b0 = t.c0 + (int)rank * half, m0 = t.m0 + (int)rank * 128;
+      const int nbox = B_MN ? (half + 63) / 64 : (half + 31) / 32;
+      const uint32_t bytes = Cfg::A_BYTES + nbox * (B_MN ? 8192 : 4096);
+      for (int kb = 0; kb < t.kbs; ++kb, ++it) {
+        const int s = it % STAGES, f = it / STAGES;
+        if (f > 0) {
+          if (lane == 0) ok = mbar_wait_cluster(&empty[s], (f - 1) & 1, abort_flag, args.status);
+          ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+          if (!ok) break;
+        }
+        uint8_t* sa = smem + (size_t)s * Cfg::STAGE;
+        uint8_t* sb = sa + Cfg::A_BYTES;
+        const bool tail = B_MN && kb == t.kbs - 1 && (t.ktail & 15);
+        const uint32_t leader_full = CTAS == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+        if (lane == 0) {
+          const uint32_t bar = tail ? smem_u32(tailbar) : leader_full;
+          if (tail) mbar_expect_tx(tailbar, bytes);
+          else if (CTAS == 2) mbar_expect_cluster(bar, bytes);
+          else mbar_expect_tx(&full[s], bytes);
+          const int k0 = kb * GT_BK;
+          if (MODE == GROUPED_FWD) {
+            tma_3d<CTAS>(sa, &mA, bar, k0, m0, t.e);
+          } else if (MODE == GROUPED_DX) {
+            tma_3d<CTAS>(sa, &mA, bar, m0, k0, t.e);
+            tma_3d<CTAS>(sa + 8192, &mA, bar, m0 + 64, k0, t.e);
+          } else {
+            tma_2d<CTAS>(sa, &mA, bar, m0, t.krow + k0);
+            tma_2d<CTAS>(sa + 8192, &mA, bar, m0 + 64, t.krow + k0);
+          }
+          if (B_MN) {
+            for (int i = 0; i < nbox; ++i) tma_2d<CTAS>(sb + i * 8192, &mB, bar, b0 + 64 * i, t.krow + k0);
+          } else if (nbox * 32 == Cfg::B_ROWS) {
+            tma_2d<CTAS>(sb, &mB, bar, k0, b0);
+          } else {
+            for (int i = 0; i < nbox; ++i) tma_2d<CTAS>(sb + i * 4096, &mB32, bar, k0, b0 + 32 * i);
+          }
+        }
+        if (tail) {
+          // The last MMA of the group takes k up to the next multiple of 16:
+          // what lies there belongs to other groups and may hold anything,
+          // so both operands are cleared from ktail on.
+          __syncwarp();
+          ok = mbar_wait(tailbar, tails++ & 1, abort_flag, args.status);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          const int k1 = (t.ktail + 15) & ~15;
+          for (int i = lane; i < (k1 - t.ktail) * 8; i += 32) {
+            const int at = t.ktail * 128 + i * 16;   // whole rows of 128 bytes: the swizzle permutes within a row
+            for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4*>(sa + c * 8192 + at) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < nbox; ++c) *reinterpret_cast<uint4*>(sb + c * 8192 + at) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (CTAS == 2) mbar_arrive_cluster(leader_full);
+            else mbar_arrive(&full[s]);
+          }
+        }
+      }
+    }
+    // after a timeout: this CTA's copies land before it can exit
+    if (!ok && lane == 0 && rank == 0) {
+      for (int s = 0; s < STAGES && s < it; ++s) {
+        const int last = s + STAGES * ((it - 1 - s) / STAGES);
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait_cluster(&full[s], (last / STAGES) & 1))
+          if (globaltimer() - t0 > SFFN_WAIT_LIMIT_NS) break;
+      }
+    }
+  } else if (warp == GT_MMA) {
+    if (lane == 0 && rank == 0) {
+      // --------------------------------------------------------- MMA issuer
+      // (of the pair: the other CTA's MMA warp only waits for the end)
+      int it = 0, ci = 0;
+      bool ok = true;
+      for (int w = walk0; w < n_tiles && ok; w += n_walk) {
+        t.set(w);
+        const uint32_t idesc = idesc_bf16_f32(128 * CTAS, t.bn) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16);
+        for (int kc = 0; kc < t.kbs && ok; kc += args.kchunk, ++ci) {
+          const int b = ci & 1;
+          if (ci >= 2 && !mbar_wait_cluster(&accfree[b], (uint32_t)(((ci >> 1) - 1) & 1), abort_flag, args.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + (uint32_t)(b * BN);
+          const int k1 = min(kc + args.kchunk, t.kbs);
+          for (int kb = kc; kb < k1; ++kb, ++it) {
+            const int s = it % STAGES, f = it / STAGES;
+            if (!mbar_wait_cluster(&full[s], f & 1, abort_flag, args.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + (size_t)s * Cfg::STAGE);
+            const uint64_t ad = A_MN ? sdesc_mn_sw128(sa, 8192) : sdesc_k_sw128(sa);
+            const uint64_t bd = B_MN ? sdesc_mn_sw128(sa + Cfg::A_BYTES, 8192) : sdesc_k_sw128(sa + Cfg::A_BYTES);
+            const int nk = kb == t.kbs - 1 ? (t.ktail + 15) / 16 : GT_BK / 16;
+            for (int k = 0; k < nk; ++k)
+              pair_mma<CTAS, false>(d, ad + (A_MN ? 128u : 2u) * k, bd + (B_MN ? 128u : 2u) * k, idesc,
+                                    (kb == kc && k == 0) ? 0u : 1u);
+            pair_commit<CTAS>(&empty[s]);
+          }
+          if (ok) pair_commit<CTAS>(&accfull[b]);
+        }
+      }
+      pair_commit<CTAS>(mma_done);
+    }
+    if (lane == 0) {
+      // every MMA of this CTA (pair) is complete before TMEM is freed
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait_cluster(mma_done, 0)) {
+        if (globaltimer() - t0 > SFFN_WAIT_LIMIT_NS) {
+          atomicOr(args.status, DEV_ERR_TIMEOUT);
+          break;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- epilogue
+    constexpr int NCH = (BN + 63) / 64;   // 32-column pieces per warpgroup
+    const int wg = warp >> 2;
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t free0 = CTAS == 2 ? cluster_addr(smem_u32(&accfree[0]), 0) : smem_u32(&accfree[0]);
+    int ci = 0;
+    bool ok = true;
+    for (int w = walk0; w < n_tiles && ok; w += n_walk) {
+      t.set(w);
+      float acc[NCH][32];
+#pragma unroll
+      for (int j = 0; j < NCH; ++j)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[j][i] = 0.0f;
+      for (int kc = 0; kc < t.kbs; kc += args.kchunk, ++ci) {
+        const int b = ci & 1;
+        // the loads from TMEM are warp-wide: all lanes go on, or none
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&accfull[b], (uint32_t)((ci >> 1) & 1), abort_flag, args.status));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+          const int c = 64 * j + 32 * wg;
+          if (c < t.cols) {
+            float v[32];
+            tmem_ld32(tlane + (uint32_t)(b * BN + c), v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[j][i] += v[i];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CTAS == 2) mbar_arrive_cluster(free0 + 8 * b);
+          else mbar_arrive(&accfree[b]);
+        }
+      }
+      if (!ok) break;
+      const int m = t.m0 + (int)rank * 128 + (warp & 3) * 32 + lane;
+      const bool in = m < t.M;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int c = 64 * j + 32 * wg;
+        if (args.out_f32) {
+          float* o = reinterpret_cast<float*>(args.out) + (t.orow + c) * (size_t)t.M + m;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (in && c + i < t.cols) o[(size_t)i * t.M] = acc[j][i];
+        } else {
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(args.out) + (t.orow + c) * (size_t)t.M + m;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (in && c + i < t.cols) o[(size_t)i * t.M] = __float2bfloat16(acc[j][i]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (CTAS == 2) cluster_sync();   // neither CTA leaves while the other may still signal or read it
+  if (warp == GT_MMA) {
+    tc_fence_after();
+    pair_tmem_dealloc<CTAS>(tmem, NCOLS);
+  }
 }
 
 }  // namespace sffn

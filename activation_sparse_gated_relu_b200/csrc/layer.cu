@@ -320,7 +320,57 @@ struct sffn_grouped_handle {
   sffn_grouped_desc desc;
   int dev = 0, n_sm = 0;
   uint32_t* status = nullptr;   // [4]
+  CUtensorMap mW, mWT;          // W as the forward's (K-major) and the input gradient's (M-major) operand
 };
+
+namespace {
+
+// Tensor map of bf16 [planes][rows][inner] (planes 0: two dimensions), box 64 x
+// box_rows, 128-byte swizzle.
+bool grouped_map(CUtensorMap* m, const void* base, long long inner, long long rows, int planes, int box_rows) {
+  const EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)inner * rows * 2};
+  const cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, 1u};
+  const cuuint32_t es[3] = {1u, 1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, int CTAS, int BN>
+cudaError_t grouped_attr() {
+  return cudaFuncSetAttribute(k_grouped<MODE, CTAS, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              GtCfg<CTAS, BN>::SMEM);
+}
+
+// One launch: the columns' operand map(s) of this call, then the kernel.
+template <int MODE, int CTAS, int BN>
+sffn_status grouped_launch(const sffn_grouped_handle* h, const CUtensorMap& mA, const void* cols, long long inner,
+                           const GroupedArgs& g, long long tiles, cudaStream_t st) {
+  CUtensorMap mB, mB32;
+  if (!grouped_map(&mB, cols, inner, g.R, 0, MODE == GROUPED_DW ? 64 : GtCfg<CTAS, BN>::B_ROWS)) return SFFN_ERR_CUDA;
+  if (MODE == GROUPED_DW) mB32 = mB;
+  else if (!grouped_map(&mB32, cols, inner, g.R, 0, 32)) return SFFN_ERR_CUDA;
+  const int grid = (int)std::min<long long>(tiles, h->n_sm / CTAS) * CTAS;
+  return launched(launch_pdl(k_grouped<MODE, CTAS, BN>, dim3(grid), dim3(GT_THREADS), (size_t)GtCfg<CTAS, BN>::SMEM, st,
+                             CTAS, mA, mB, mB32, g));
+}
+
+// Products over the rows of every group (forward, input gradient).
+template <int MODE>
+sffn_status grouped_rows(const sffn_grouped_handle* h, const CUtensorMap& mA, const void* rows, const GroupedArgs& g,
+                         cudaStream_t st) {
+  // tiles of 256 columns are at most R / 256 + E; their count is an int
+  const long long tiles = (long long)cdiv(g.M, 128) * (g.R / 32 + g.E);
+  if (tiles > 0x7FFFFFFFll) return SFFN_ERR_UNSUPPORTED;
+  if (g.R >= 96ll * g.E) return grouped_launch<MODE, 2, 256>(h, mA, rows, g.K, g, tiles, st);
+  if (g.R >= 24ll * g.E) return grouped_launch<MODE, 1, 128>(h, mA, rows, g.K, g, tiles, st);
+  return grouped_launch<MODE, 1, 32>(h, mA, rows, g.K, g, tiles, st);
+}
+
+}  // namespace
 
 extern "C" sffn_status sffn_grouped_create(const sffn_grouped_desc* desc, void* cuda_stream, sffn_grouped_handle** out) {
   if (!out) return SFFN_ERR_INVALID_ARG;
@@ -343,9 +393,21 @@ extern "C" sffn_status sffn_grouped_create(const sffn_grouped_desc* desc, void* 
     delete h;
     return SFFN_ERR_ALLOC;
   }
+  const int E = desc->n_experts;
   cudaError_t e = cudaMemsetAsync(h->status, 0, 16, st);
+  if (!e && (!grouped_map(&h->mW, desc->W, desc->d_in, desc->d_out, E, 128) ||
+             !grouped_map(&h->mWT, desc->W, desc->d_in, desc->d_out, E, 64)))
+    e = cudaErrorInvalidValue;
+  e = e ? e : grouped_attr<GROUPED_FWD, 2, 256>();
+  e = e ? e : grouped_attr<GROUPED_FWD, 1, 128>();
+  e = e ? e : grouped_attr<GROUPED_FWD, 1, 32>();
+  e = e ? e : grouped_attr<GROUPED_DX, 2, 256>();
+  e = e ? e : grouped_attr<GROUPED_DX, 1, 128>();
+  e = e ? e : grouped_attr<GROUPED_DX, 1, 32>();
+  e = e ? e : grouped_attr<GROUPED_DW, 2, 256>();
   e = e ? e : cudaStreamSynchronize(st);
   if (e) {
+    cudaGetLastError();
     free_on(dev, h->status);
     delete h;
     return SFFN_ERR_CUDA;
@@ -364,15 +426,18 @@ sffn_status grouped_check(const sffn_grouped_handle* h, const void* a, const int
   return on_device(h->dev) ? SFFN_OK : SFFN_ERR_INVALID_ARG;
 }
 
+// fp32 outputs: the tensor core's own sum keeps fewer bits than an fp32 sum
+// rounded to nearest (relative error 4e-6 over 4096 terms, 5e-7 over 512), so
+// runs of 512 terms (8 blocks) are added up in registers.  A bf16 output's
+// rounding is a thousand times that.
 GroupedArgs grouped_args(const sffn_grouped_handle* h, const int32_t* offsets, int R, void* out, int out_dtype) {
   GroupedArgs g{};
   g.off = offsets;
   g.out = out;
   g.E = h->desc.n_experts;
   g.R = R;
-  g.k = h->desc.d_in;
-  g.n = h->desc.d_out;
   g.out_f32 = out_dtype == SFFN_FP32;
+  g.kchunk = g.out_f32 ? 8 : 1 << 30;
   g.status = h->status;
   return g;
 }
@@ -384,10 +449,9 @@ extern "C" sffn_status sffn_grouped_forward(sffn_grouped_handle* h, const void* 
   const sffn_status s = grouped_check(h, x, offsets, R, y, y_dtype);
   if (s != SFFN_OK || R == 0) return s;
   GroupedArgs g = grouped_args(h, offsets, R, y, y_dtype);
-  g.a = static_cast<const __nv_bfloat16*>(x);
-  g.b = static_cast<const __nv_bfloat16*>(h->desc.W);
-  return launched(launch_pdl(k_grouped_rows<0>, dim3(cdiv(g.n, 32), g.E), dim3(256), 0,
-                             static_cast<cudaStream_t>(cuda_stream), 1, g));
+  g.M = h->desc.d_out;
+  g.K = h->desc.d_in;
+  return grouped_rows<GROUPED_FWD>(h, h->mW, x, g, static_cast<cudaStream_t>(cuda_stream));
 }
 
 extern "C" sffn_status sffn_grouped_backward_input(sffn_grouped_handle* h, const void* dy, const int32_t* offsets, int R,
@@ -395,10 +459,9 @@ extern "C" sffn_status sffn_grouped_backward_input(sffn_grouped_handle* h, const
   const sffn_status s = grouped_check(h, dy, offsets, R, dx, dx_dtype);
   if (s != SFFN_OK || R == 0) return s;
   GroupedArgs g = grouped_args(h, offsets, R, dx, dx_dtype);
-  g.a = static_cast<const __nv_bfloat16*>(dy);
-  g.b = static_cast<const __nv_bfloat16*>(h->desc.W);
-  return launched(launch_pdl(k_grouped_rows<1>, dim3(cdiv(g.k, 32), g.E), dim3(256), 0,
-                             static_cast<cudaStream_t>(cuda_stream), 1, g));
+  g.M = h->desc.d_in;
+  g.K = h->desc.d_out;
+  return grouped_rows<GROUPED_DX>(h, h->mWT, dy, g, static_cast<cudaStream_t>(cuda_stream));
 }
 
 extern "C" sffn_status sffn_grouped_backward_weight(sffn_grouped_handle* h, const void* x, const void* dy,
@@ -407,11 +470,17 @@ extern "C" sffn_status sffn_grouped_backward_weight(sffn_grouped_handle* h, cons
   const sffn_status s = grouped_check(h, x, offsets, R, dW, dw_dtype);
   if (s != SFFN_OK) return s;
   if (!dW || !aligned16(dW) || (R > 0 && (!dy || !aligned16(dy)))) return SFFN_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   GroupedArgs g = grouped_args(h, offsets, R, dW, dw_dtype);
-  g.a = static_cast<const __nv_bfloat16*>(dy);
-  g.b = static_cast<const __nv_bfloat16*>(x);
-  return launched(launch_pdl(k_grouped_weight, dim3(cdiv(g.k, 32), cdiv(g.n, 8), g.E), dim3(256), 0,
-                             static_cast<cudaStream_t>(cuda_stream), 1, g));
+  g.M = h->desc.d_in;
+  g.N = h->desc.d_out;
+  if (R == 0)
+    return launched(cudaMemsetAsync(dW, 0, (size_t)g.E * g.M * g.N * (g.out_f32 ? 4 : 2), st));
+  CUtensorMap mx;
+  if (!grouped_map(&mx, x, g.M, R, 0, 64)) return SFFN_ERR_CUDA;
+  const long long tiles = (long long)g.E * cdiv(g.M, 256) * cdiv(g.N, 256);
+  if (tiles > 0x7FFFFFFFll) return SFFN_ERR_UNSUPPORTED;
+  return grouped_launch<GROUPED_DW, 2, 256>(h, mx, dy, g.N, g, tiles, st);
 }
 
 extern "C" sffn_status sffn_grouped_read_status(sffn_grouped_handle* h, void* cuda_stream) {
