@@ -212,16 +212,13 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
       const uint32_t bytes = Cfg::A_BYTES + nbox * (B_MN ? 8192 : 4096);
       for (int kb = 0; kb < t.kbs; ++kb, ++it) {
         const int s = it % STAGES, f = it / STAGES;
-        if (f > 0) {
-          if (lane == 0) ok = mbar_wait_cluster(&empty[s], (f - 1) & 1, abort_flag, args.status);
-          ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
-          if (!ok) break;
-        }
+        if (f > 0) ok = mbar_wait_warp(&empty[s], (f - 1) & 1, abort_flag, args.status);
+        if (!ok) break;
         uint8_t* sa = smem + (size_t)s * Cfg::STAGE;
         uint8_t* sb = sa + Cfg::A_BYTES;
         const bool tail = B_MN && kb == t.kbs - 1 && (t.ktail & 15);
         const uint32_t leader_full = CTAS == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t bar = tail ? smem_u32(tailbar) : leader_full;
           if (tail) mbar_expect_tx(tailbar, bytes);
           else if (CTAS == 2) mbar_expect_cluster(bar, bytes);
@@ -249,8 +246,7 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
           // what lies there belongs to other groups and may hold anything,
           // so both operands are cleared from ktail on.
           __syncwarp();
-          ok = mbar_wait(tailbar, tails++ & 1, abort_flag, args.status);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+          ok = mbar_wait_warp(tailbar, tails++ & 1, abort_flag, args.status);
           const int k1 = (t.ktail + 15) & ~15;
           for (int i = lane; i < (k1 - t.ktail) * 8; i += 32) {
             const int at = t.ktail * 128 + i * 16;   // whole rows of 128 bytes: the swizzle permutes within a row
@@ -260,7 +256,7 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (CTAS == 2) mbar_arrive_cluster(leader_full);
+            if (CTAS == 2) mbar_release_cluster(leader_full);
             else mbar_arrive(&full[s]);
           }
         }
@@ -271,12 +267,12 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
       for (int s = 0; s < STAGES && s < it; ++s) {
         const int last = s + STAGES * ((it - 1 - s) / STAGES);
         const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait_cluster(&full[s], (last / STAGES) & 1))
+        while (!mbar_try_wait(&full[s], (last / STAGES) & 1))
           if (globaltimer() - t0 > SFFN_WAIT_LIMIT_NS) break;
       }
     }
   } else if (warp == GT_MMA) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // --------------------------------------------------------- MMA issuer
       // (of the pair: the other CTA's MMA warp only waits for the end)
       int it = 0, ci = 0;
@@ -286,38 +282,41 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         const uint32_t idesc = idesc_bf16_f32(128 * CTAS, t.bn) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16);
         for (int kc = 0; kc < t.kbs && ok; kc += args.kchunk, ++ci) {
           const int b = ci & 1;
-          if (ci >= 2 && !mbar_wait_cluster(&accfree[b], (uint32_t)(((ci >> 1) - 1) & 1), abort_flag, args.status)) {
-            ok = false;
-            break;
-          }
+          if (ci >= 2) ok = mbar_wait_warp(&accfree[b], (uint32_t)(((ci >> 1) - 1) & 1), abort_flag, args.status);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + (uint32_t)(b * BN);
           const int k1 = min(kc + args.kchunk, t.kbs);
           for (int kb = kc; kb < k1; ++kb, ++it) {
             const int s = it % STAGES, f = it / STAGES;
-            if (!mbar_wait_cluster(&full[s], f & 1, abort_flag, args.status)) {
-              ok = false;
-              break;
-            }
+            ok = mbar_wait_warp(&full[s], f & 1, abort_flag, args.status);
+            if (!ok) break;
             tc_fence_after();
             const uint32_t sa = smem_u32(smem + (size_t)s * Cfg::STAGE);
             const uint64_t ad = A_MN ? sdesc_mn_sw128(sa, 8192) : sdesc_k_sw128(sa);
             const uint64_t bd = B_MN ? sdesc_mn_sw128(sa + Cfg::A_BYTES, 8192) : sdesc_k_sw128(sa + Cfg::A_BYTES);
             const int nk = kb == t.kbs - 1 ? (t.ktail + 15) / 16 : GT_BK / 16;
-            for (int k = 0; k < nk; ++k)
-              pair_mma<CTAS, false>(d, ad + (A_MN ? 128u : 2u) * k, bd + (B_MN ? 128u : 2u) * k, idesc,
-                                    (kb == kc && k == 0) ? 0u : 1u);
-            pair_commit<CTAS>(&empty[s]);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < GT_BK / 16; ++k)
+                if (k < nk)
+                  pair_mma<CTAS, false>(d, ad + (A_MN ? 128u : 2u) * k, bd + (B_MN ? 128u : 2u) * k, idesc,
+                                        (kb == kc && k == 0) ? 0u : 1u);
+              pair_commit<CTAS>(&empty[s]);
+            }
+            __syncwarp();
           }
-          if (ok) pair_commit<CTAS>(&accfull[b]);
+          if (ok && elect_one()) pair_commit<CTAS>(&accfull[b]);
+          __syncwarp();
         }
       }
-      pair_commit<CTAS>(mma_done);
+      if (elect_one()) pair_commit<CTAS>(mma_done);
+      __syncwarp();
     }
     if (lane == 0) {
       // every MMA of this CTA (pair) is complete before TMEM is freed
       const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait_cluster(mma_done, 0)) {
+      while (!mbar_try_wait(mma_done, 0)) {
         if (globaltimer() - t0 > SFFN_WAIT_LIMIT_NS) {
           atomicOr(args.status, DEV_ERR_TIMEOUT);
           break;
@@ -342,7 +341,7 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
       for (int kc = 0; kc < t.kbs; kc += args.kchunk, ++ci) {
         const int b = ci & 1;
         // the loads from TMEM are warp-wide: all lanes go on, or none
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&accfull[b], (uint32_t)((ci >> 1) & 1), abort_flag, args.status));
+        ok = mbar_wait_warp(&accfull[b], (uint32_t)((ci >> 1) & 1), abort_flag, args.status);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
