@@ -334,10 +334,6 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
     for (int w = walk0; w < n_tiles && ok; w += n_walk) {
       t.set(w);
       float acc[NCH][32];
-#pragma unroll
-      for (int j = 0; j < NCH; ++j)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[j][i] = 0.0f;
       for (int kc = 0; kc < t.kbs; kc += args.kchunk, ++ci) {
         const int b = ci & 1;
         // the loads from TMEM are warp-wide: all lanes go on, or none
@@ -348,10 +344,14 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         for (int j = 0; j < NCH; ++j) {
           const int c = 64 * j + 32 * wg;
           if (c < t.cols) {
-            float v[32];
-            tmem_ld32(tlane + (uint32_t)(b * BN + c), v);
+            if (kc == 0) {
+              tmem_ld32(tlane + (uint32_t)(b * BN + c), acc[j]);
+            } else {
+              float v[32];
+              tmem_ld32(tlane + (uint32_t)(b * BN + c), v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[j][i] += v[i];
+              for (int i = 0; i < 32; ++i) acc[j][i] += v[i];
+            }
           }
         }
         tc_fence_before();
@@ -362,21 +362,42 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         }
       }
       if (!ok) break;
+      if (MODE == GROUPED_DW && t.kbs == 0) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[j][i] = 0.0f;
+      }
       const int m = t.m0 + (int)rank * 128 + (warp & 3) * 32 + lane;
-      const bool in = m < t.M;
+      if (m < t.M) {   // M is a multiple of 8: both lanes of a pair are in, or neither
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) {
-        const int c = 64 * j + 32 * wg;
-        if (args.out_f32) {
-          float* o = reinterpret_cast<float*>(args.out) + (t.orow + c) * (size_t)t.M + m;
+        for (int j = 0; j < NCH; ++j) {
+          const int c = 64 * j + 32 * wg, n = t.cols - c;
+          if (n <= 0) break;
+          if (args.out_f32) {
+            float* o = reinterpret_cast<float*>(args.out) + (t.orow + c) * (size_t)t.M + m;
+            if (n >= 32) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (in && c + i < t.cols) o[(size_t)i * t.M] = acc[j][i];
-        } else {
-          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(args.out) + (t.orow + c) * (size_t)t.M + m;
+              for (int i = 0; i < 32; ++i, o += t.M) *o = acc[j][i];
+            } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (in && c + i < t.cols) o[(size_t)i * t.M] = __float2bfloat16(acc[j][i]);
+              for (int i = 0; i < 32; ++i, o += t.M)
+                if (i < n) *o = acc[j][i];
+            }
+          } else {
+            // two columns at a time: even lanes store two rows m of the first
+            // one, odd lanes of the second
+            const int odd = lane & 1;
+            const uint32_t sel = odd ? 0x3276u : 0x5410u;
+            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(args.out) + (t.orow + c + odd) * (size_t)t.M + (m - odd);
+            const unsigned mask = __activemask();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2, o += 2 * (size_t)t.M) {
+              const uint32_t p = pack_bf16(acc[j][i], acc[j][i + 1]);
+              const uint32_t q = __shfl_xor_sync(mask, p, 1);
+              if (i + odd < n) *reinterpret_cast<uint32_t*>(o) = __byte_perm(p, q, sel);
+            }
+          }
         }
       }
     }
