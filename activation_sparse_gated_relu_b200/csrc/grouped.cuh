@@ -33,7 +33,8 @@ enum { GROUPED_FWD = 0, GROUPED_DX = 1, GROUPED_DW = 2 };
 constexpr int GROUPED_MAX_E = 1024;
 constexpr int GT_EPI_WARPS = 8;                        // two warpgroups, every other 32 columns each
 constexpr int GT_PRODUCER = GT_EPI_WARPS, GT_MMA = GT_EPI_WARPS + 1;
-constexpr int GT_THREADS = (GT_EPI_WARPS + 2) * 32;
+constexpr int GT_FIX = GT_EPI_WARPS + 2;              // clears what lies behind a group's end (weight gradient)
+constexpr int GT_THREADS = (GT_EPI_WARPS + 3) * 32;
 constexpr int GT_BK = 64;                              // bf16 values of k per stage
 constexpr int GT_SMEM = 227 * 1024;
 
@@ -45,7 +46,7 @@ struct GtCfg {
   static constexpr int B_BYTES = B_ROWS * GT_BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int TABLE = (3 * (GROUPED_MAX_E + 1) * 4 + 127) & ~127;
-  static constexpr int FIXED = 1024 /*align*/ + 256 /*barriers*/ + TABLE;
+  static constexpr int FIXED = 1024 /*align*/ + 384 /*barriers*/ + TABLE;
   static constexpr int RAW = (GT_SMEM - FIXED) / STAGE;
   static constexpr int STAGES = RAW > 10 ? 10 : RAW;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
@@ -128,12 +129,12 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   uint64_t* empty = full + STAGES;
   uint64_t* accfull = empty + STAGES;   // [2]
   uint64_t* accfree = accfull + 2;      // [2]
-  uint64_t* tailbar = accfree + 2;
-  uint64_t* mma_done = tailbar + 1;
+  uint64_t* tailbar = accfree + 2;      // [STAGES] a group's last block has landed, not yet cleared
+  uint64_t* mma_done = tailbar + STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * STAGES + 6) * 8 + 8 <= 256, "barrier area");
-  int* ra = reinterpret_cast<int*>(smem + STAGES * Cfg::STAGE + 256);
+  static_assert((3 * STAGES + 5) * 8 + 8 <= 384, "barrier area");
+  int* ra = reinterpret_cast<int*>(smem + STAGES * Cfg::STAGE + 384);
   int* rb = ra + GROUPED_MAX_E + 1;
   int* first = rb + GROUPED_MAX_E + 1;
 
@@ -145,12 +146,12 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], CTAS);        // one arrival per CTA's producer
       mbar_init(&empty[s], 1);
+      mbar_init(&tailbar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
       mbar_init(&accfree[b], GT_EPI_WARPS * CTAS);
     }
-    mbar_init(tailbar, 1);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -201,9 +202,7 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
 
   if (warp == GT_PRODUCER) {
     // --------------------------------------------------------- TMA producer
-    // The whole warp walks along, so that its lanes can clear the rows behind
-    // a group's end.
-    int it = 0, tails = 0;
+    int it = 0;
     bool ok = true;
     for (int w = walk0; w < n_tiles && ok; w += n_walk) {
       t.set(w);
@@ -219,8 +218,8 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         const bool tail = B_MN && kb == t.kbs - 1 && (t.ktail & 15);
         const uint32_t leader_full = CTAS == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
         if (elect_one()) {
-          const uint32_t bar = tail ? smem_u32(tailbar) : leader_full;
-          if (tail) mbar_expect_tx(tailbar, bytes);
+          const uint32_t bar = tail ? smem_u32(&tailbar[s]) : leader_full;
+          if (tail) mbar_expect_tx(&tailbar[s], bytes);
           else if (CTAS == 2) mbar_expect_cluster(bar, bytes);
           else mbar_expect_tx(&full[s], bytes);
           const int k0 = kb * GT_BK;
@@ -241,34 +240,43 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
             for (int i = 0; i < nbox; ++i) tma_2d<CTAS>(sb + i * 4096, &mB32, bar, k0, b0 + 32 * i);
           }
         }
-        if (tail) {
-          // The last MMA of the group takes k up to the next multiple of 16:
-          // what lies there belongs to other groups and may hold anything,
-          // so both operands are cleared from ktail on.
-          __syncwarp();
-          ok = mbar_wait_warp(tailbar, tails++ & 1, abort_flag, args.status);
-          const int k1 = (t.ktail + 15) & ~15;
-          for (int i = lane; i < (k1 - t.ktail) * 8; i += 32) {
-            const int at = t.ktail * 128 + i * 16;   // whole rows of 128 bytes: the swizzle permutes within a row
-            for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4*>(sa + c * 8192 + at) = make_uint4(0, 0, 0, 0);
-            for (int c = 0; c < nbox; ++c) *reinterpret_cast<uint4*>(sb + c * 8192 + at) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (CTAS == 2) mbar_release_cluster(leader_full);
-            else mbar_arrive(&full[s]);
-          }
-        }
       }
     }
-    // after a timeout: this CTA's copies land before it can exit
-    if (!ok && lane == 0 && rank == 0) {
-      for (int s = 0; s < STAGES && s < it; ++s) {
-        const int last = s + STAGES * ((it - 1 - s) / STAGES);
-        const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(&full[s], (last / STAGES) & 1))
-          if (globaltimer() - t0 > SFFN_WAIT_LIMIT_NS) break;
+    // After a timeout the CTA must not exit before its copies have landed.
+    // Their barriers may be the other CTA's or half-armed, so it waits the
+    // time that any copy takes many times over.
+    if (!ok) {
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
+    }
+  } else if (warp == GT_FIX) {
+    // --------------------------------------------------- weight gradient only
+    // The last MMA of a group takes k up to the next multiple of 16: what lies
+    // there belongs to other groups and may hold anything, so both operands
+    // are cleared from ktail on before the MMA warp sees the stage.
+    int it = 0;
+    uint32_t used = 0;                  // parity of tailbar[s] in bit s
+    for (int w = walk0; B_MN && w < n_tiles; w += n_walk) {
+      t.set(w);
+      it += t.kbs;
+      if (t.kbs == 0 || !(t.ktail & 15)) continue;
+      const int s = (it - 1) % STAGES;
+      if (!mbar_wait_warp(&tailbar[s], (used >> s) & 1, abort_flag, args.status)) break;
+      used ^= 1u << s;
+      uint8_t* sa = smem + (size_t)s * Cfg::STAGE;
+      uint8_t* sb = sa + Cfg::A_BYTES;
+      const int nbox = (t.bn / CTAS + 63) / 64;
+      const int k1 = (t.ktail + 15) & ~15;
+      for (int i = lane; i < (k1 - t.ktail) * 8; i += 32) {
+        const int at = t.ktail * 128 + i * 16;   // whole rows of 128 bytes: the swizzle permutes within a row
+        for (int c = 0; c < 2; ++c) *reinterpret_cast<uint4*>(sa + c * 8192 + at) = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < nbox; ++c) *reinterpret_cast<uint4*>(sb + c * 8192 + at) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (CTAS == 2) mbar_release_cluster(cluster_addr(smem_u32(&full[s]), 0));
+        else mbar_arrive(&full[s]);
       }
     }
   } else if (warp == GT_MMA) {
