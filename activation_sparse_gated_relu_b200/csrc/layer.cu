@@ -251,6 +251,41 @@ struct sffn_qlinear_handle {
   uint32_t* status = nullptr;   // [4]
 };
 
+namespace {
+
+// Tensor map of e4m3 codes [rows][inner], box 128 x box_rows, 128-byte swizzle.
+bool code_map(CUtensorMap* m, const void* base, long long inner, long long rows, int box_rows) {
+  const EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)inner};
+  const cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+  const cuuint32_t es[2] = {1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+cudaError_t qlinear_cols_attr() {
+  return cudaFuncSetAttribute(k_qlinear_cols<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, QcCfg<BN>::SMEM);
+}
+
+template <int BN>
+sffn_status qlinear_cols(const sffn_qlinear_handle* h, const void* xq, QlinArgs a, cudaStream_t st) {
+  const int nt = cdiv(a.T, BN);
+  a.each = cdiv(cdiv(a.T, nt), 16) * 16;
+  // as many tiles as SMs, of the same height: fewer rows per CTA than 128 where
+  // the weight has few
+  a.h = std::min(128, std::max(8, cdiv(cdiv((long long)a.n * nt, h->n_sm), 8) * 8));
+  CUtensorMap mW, mX;
+  if (!code_map(&mW, h->desc.Wq, a.k, a.n, a.h) || !code_map(&mX, xq, a.k, a.T, a.each)) return SFFN_ERR_CUDA;
+  return launched(launch_pdl(k_qlinear_cols<BN>, dim3(cdiv(a.n, a.h), nt), dim3(QL_THREADS), (size_t)QcCfg<BN>::SMEM, st,
+                             1, mW, mX, a));
+}
+
+}  // namespace
+
 extern "C" sffn_status sffn_qlinear_create(const sffn_qlinear_desc* desc, void* cuda_stream, sffn_qlinear_handle** out) {
   if (!out) return SFFN_ERR_INVALID_ARG;
   *out = nullptr;
@@ -271,8 +306,14 @@ extern "C" sffn_status sffn_qlinear_create(const sffn_qlinear_desc* desc, void* 
     return SFFN_ERR_ALLOC;
   }
   cudaError_t e = cudaMemsetAsync(h->status, 0, 16, st);
+  e = e ? e : qlinear_cols_attr<16>();
+  e = e ? e : qlinear_cols_attr<32>();
+  e = e ? e : qlinear_cols_attr<64>();
+  e = e ? e : qlinear_cols_attr<128>();
+  e = e ? e : qlinear_cols_attr<256>();
   e = e ? e : cudaStreamSynchronize(st);
-  if (e) {
+  if (e || !get_encode()) {
+    cudaGetLastError();
     free_on(dev, h->status);
     delete h;
     return SFFN_ERR_CUDA;
@@ -288,9 +329,7 @@ extern "C" sffn_status sffn_qlinear_forward(sffn_qlinear_handle* h, const void* 
   if (!xq || !xs || !y || !aligned16(xq) || !aligned16(xs) || !aligned16(y)) return SFFN_ERR_INVALID_ARG;
   if (!on_device(h->dev)) return SFFN_ERR_INVALID_ARG;
   QlinArgs a{};
-  a.xq = static_cast<const uint8_t*>(xq);
   a.xs = xs;
-  a.Wq = static_cast<const uint8_t*>(h->desc.Wq);
   a.Ws = h->desc.Ws;
   a.y = y;
   a.T = T;
@@ -299,8 +338,13 @@ extern "C" sffn_status sffn_qlinear_forward(sffn_qlinear_handle* h, const void* 
   a.kb = cdiv(a.k, Q_GROUP);
   a.y_f32 = y_dtype == SFFN_FP32;
   a.status = h->status;
-  return launched(launch_pdl(k_qlinear, dim3(cdiv(a.n, 32), cdiv(T, 8)), dim3(256), 0,
-                             static_cast<cudaStream_t>(cuda_stream), 1, a));
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (cdiv(T, 256) > 65535) return SFFN_ERR_UNSUPPORTED;
+  if (T <= 16) return qlinear_cols<16>(h, xq, a, st);
+  if (T <= 32) return qlinear_cols<32>(h, xq, a, st);
+  if (T <= 64) return qlinear_cols<64>(h, xq, a, st);
+  if (T <= 128) return qlinear_cols<128>(h, xq, a, st);
+  return qlinear_cols<256>(h, xq, a, st);
 }
 
 extern "C" sffn_status sffn_qlinear_read_status(sffn_qlinear_handle* h, void* cuda_stream) {
