@@ -282,7 +282,7 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   } else if (warp == GT_MMA) {
     if (rank == 0) {
       // --------------------------------------------------------- MMA issuer
-      // (of the pair: the other CTA's MMA warp only waits for the end)
+      // (of the pair's first CTA)
       int it = 0, ci = 0;
       bool ok = true;
       for (int w = walk0; w < n_tiles && ok; w += n_walk) {
@@ -320,16 +320,6 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
       }
       if (elect_one()) pair_commit<CTAS>(mma_done);
       __syncwarp();
-    }
-    if (lane == 0) {
-      // every MMA of this CTA (pair) is complete before TMEM is freed
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(mma_done, 0)) {
-        if (globaltimer() - t0 > SFFN_WAIT_LIMIT_NS) {
-          atomicOr(args.status, DEV_ERR_TIMEOUT);
-          break;
-        }
-      }
     }
   } else {
     // ------------------------------------------------------------- epilogue
@@ -413,6 +403,9 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  // every MMA of this CTA (pair) is complete before TMEM is freed
+  if (warp == GT_MMA) mbar_wait_warp(mma_done, 0, abort_flag, args.status);
+  __syncwarp();
   if (CTAS == 2) cluster_sync();   // neither CTA leaves while the other may still signal or read it
   if (warp == GT_MMA) {
     tc_fence_after();

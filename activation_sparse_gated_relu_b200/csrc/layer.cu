@@ -273,15 +273,43 @@ cudaError_t qlinear_cols_attr() {
 
 template <int BN>
 sffn_status qlinear_cols(const sffn_qlinear_handle* h, const void* xq, QlinArgs a, cudaStream_t st) {
-  const int nt = cdiv(a.T, BN);
-  a.each = cdiv(cdiv(a.T, nt), 16) * 16;
-  // as many tiles as SMs, of the same height: fewer rows per CTA than 128 where
-  // the weight has few
-  a.h = std::min(128, std::max(8, cdiv(cdiv((long long)a.n * nt, h->n_sm), 8) * 8));
+  a.each = cdiv(a.T, 16) * 16;
+  // One tile per SM: tiles of 128 weight rows, cut along k over up to 8 CTAs
+  // where they leave SMs idle, then rows per tile evened out over what is left.
+  const int nt = cdiv(a.n, 128);
+  a.split = 1;
+  while (a.split < 8 && nt * a.split * 2 <= h->n_sm && a.kb >= 8 * a.split) a.split *= 2;
+  a.h = std::min(128, std::max(8, cdiv(cdiv((long long)a.n * a.split, h->n_sm), 8) * 8));
   CUtensorMap mW, mX;
   if (!code_map(&mW, h->desc.Wq, a.k, a.n, a.h) || !code_map(&mX, xq, a.k, a.T, a.each)) return SFFN_ERR_CUDA;
-  return launched(launch_pdl(k_qlinear_cols<BN>, dim3(cdiv(a.n, a.h), nt), dim3(QL_THREADS), (size_t)QcCfg<BN>::SMEM, st,
-                             1, mW, mX, a));
+  return launched(launch_pdl(k_qlinear_cols<BN>, dim3(cdiv(a.n, a.h) * a.split), dim3(QL_THREADS), (size_t)QcCfg<BN>::SMEM,
+                             st, a.split, mW, mX, a));
+}
+
+template <int CTAS>
+cudaError_t qlinear_rows_attr() {
+  return cudaFuncSetAttribute(k_qlinear_rows<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, QrCfg<CTAS>::SMEM);
+}
+
+template <int CTAS>
+sffn_status qlinear_rows(const sffn_qlinear_handle* h, const void* xq, QlinArgs a, cudaStream_t st) {
+  const long long mt = cdiv(a.T, 128 * CTAS), slots = h->n_sm / CTAS;
+  // columns per tile: what gives the least rounds x columns (a tile also costs
+  // about 32 columns' time whatever its width)
+  long long best = -1;
+  for (int n = 256; n >= 64; n -= 32) {
+    const long long cost = ((mt * cdiv(a.n, n) + slots - 1) / slots) * (n + 32);
+    if (best < 0 || cost < best) {
+      best = cost;
+      a.each = n;
+    }
+  }
+  const long long tiles = mt * cdiv(a.n, a.each);
+  if (tiles > 0x7FFFFFFFll) return SFFN_ERR_UNSUPPORTED;
+  CUtensorMap mX, mW;
+  if (!code_map(&mX, xq, a.k, a.T, 128) || !code_map(&mW, h->desc.Wq, a.k, a.n, a.each / CTAS)) return SFFN_ERR_CUDA;
+  return launched(launch_pdl(k_qlinear_rows<CTAS>, dim3((unsigned)std::min(tiles, slots) * CTAS), dim3(QR_THREADS),
+                             (size_t)QrCfg<CTAS>::SMEM, st, CTAS, mX, mW, a));
 }
 
 }  // namespace
@@ -310,7 +338,8 @@ extern "C" sffn_status sffn_qlinear_create(const sffn_qlinear_desc* desc, void* 
   e = e ? e : qlinear_cols_attr<32>();
   e = e ? e : qlinear_cols_attr<64>();
   e = e ? e : qlinear_cols_attr<128>();
-  e = e ? e : qlinear_cols_attr<256>();
+  e = e ? e : qlinear_rows_attr<1>();
+  e = e ? e : qlinear_rows_attr<2>();
   e = e ? e : cudaStreamSynchronize(st);
   if (e || !get_encode()) {
     cudaGetLastError();
@@ -339,12 +368,12 @@ extern "C" sffn_status sffn_qlinear_forward(sffn_qlinear_handle* h, const void* 
   a.y_f32 = y_dtype == SFFN_FP32;
   a.status = h->status;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  if (cdiv(T, 256) > 65535) return SFFN_ERR_UNSUPPORTED;
   if (T <= 16) return qlinear_cols<16>(h, xq, a, st);
   if (T <= 32) return qlinear_cols<32>(h, xq, a, st);
   if (T <= 64) return qlinear_cols<64>(h, xq, a, st);
   if (T <= 128) return qlinear_cols<128>(h, xq, a, st);
-  return qlinear_cols<256>(h, xq, a, st);
+  if (T <= 384) return qlinear_rows<1>(h, xq, a, st);
+  return qlinear_rows<2>(h, xq, a, st);
 }
 
 extern "C" sffn_status sffn_qlinear_read_status(sffn_qlinear_handle* h, void* cuda_stream) {

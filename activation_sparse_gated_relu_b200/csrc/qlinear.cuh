@@ -9,10 +9,15 @@
 //
 // k_qlinear_cols: few tokens.  Weight rows are the MMA's 128 rows (TMEM
 // lanes), tokens its columns, so that a token costs little and W is read
-// once.  Bound by W's bytes.  A CTA takes `h` weight rows (a multiple of 8, up
-// to 128) over all of k, with h chosen to give every SM one tile: a tile of
-// fewer rows leaves lanes of the MMA unused, which costs nothing here, and
-// needs no sum over CTAs.
+// once.  Bound by W's bytes.  An MMA of 128 x 16 x 32 takes 45 cycles however
+// many of its rows are used, and looking at a barrier 50 to 100, so a stage is
+// several blocks with one barrier each way, and a narrow weight (few rows,
+// long k) is cut along k over the CTAs of a cluster, which add their sums up
+// through distributed shared memory in a fixed order.
+//
+// k_qlinear_rows: many tokens.  Tokens are the MMA's rows, so that a token's
+// scale is one register per thread; CTA pairs share a tile of 256 tokens.
+// Bound by the tensor cores.
 #pragma once
 
 #include "ptx_pair.cuh"
@@ -56,14 +61,20 @@ struct QlinArgs {
   void* y;              // [T][n], bf16 or fp32
   int T, n, k, kb;
   int h;                // k_qlinear_cols: weight rows per CTA
-  int each;             // k_qlinear_cols: tokens per CTA (a multiple of 16)
+  int each;             // tokens per CTA (k_qlinear_cols, a multiple of 16), columns per tile (k_qlinear_rows)
+  int split;            // k_qlinear_cols: CTAs of a cluster, each with a part of k
   int y_f32;
   uint32_t* status;
 };
 
+__device__ __forceinline__ void put_y(void* y, int f32, size_t at, float v) {
+  if (f32) reinterpret_cast<float*>(y)[at] = v;
+  else reinterpret_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16(v);
+}
+
 template <int BN>
 struct QcCfg {
-  static constexpr int KS = BN <= 64 ? 2 : 1;            // 128-wide blocks per stage
+  static constexpr int KS = BN <= 32 ? 4 : BN <= 64 ? 2 : 1;   // 128-wide blocks per stage
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = KS * (A_BYTES + B_BYTES);
   static constexpr int SCALES = KS * BN * 4;             // a stage's xs, [KS][BN]
@@ -71,8 +82,8 @@ struct QcCfg {
   static constexpr int RAW = (QL_SMEM - FIXED) / (STAGE + SCALES);
   static constexpr int STAGES = RAW > 8 ? 8 : RAW;
   static constexpr int SMEM = FIXED + STAGES * (STAGE + SCALES);
-  static constexpr int NBUF = BN <= 64 ? 4 : 2;          // TMEM accumulators
-  // Up to 64 columns the two epilogue warpgroups take every other block, above
+  static constexpr int NBUF = 4;                         // TMEM accumulators, KS · BN columns each
+  // Up to 64 columns the two epilogue warpgroups take every other stage, above
   // that they halve the columns.
   static constexpr bool ALT = BN <= 64;
   static constexpr int COLS = ALT ? BN : BN / 2;         // columns per epilogue thread
@@ -83,7 +94,7 @@ __global__ void __launch_bounds__(QL_THREADS, 1)
 k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX, const QlinArgs a) {
   using Cfg = QcCfg<BN>;
   constexpr int STAGES = Cfg::STAGES, KS = Cfg::KS, NBUF = Cfg::NBUF;
-  constexpr uint32_t NCOLS = NBUF * BN;
+  constexpr uint32_t NCOLS = NBUF * KS * BN;
   static_assert(NCOLS >= 32 && NCOLS <= 512 && (NCOLS & (NCOLS - 1)) == 0, "TMEM columns");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -100,16 +111,19 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   static_assert((4 * STAGES + 2 * NBUF + 1) * 8 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int m0 = blockIdx.x * a.h, n0 = blockIdx.y * a.each;
+  const int rank = a.split > 1 ? (int)cluster_rank() : 0;
+  const int m0 = (blockIdx.x / a.split) * a.h, n0 = blockIdx.y * a.each;
   const int cols = min(a.each, a.T - n0), bn = (cols + 15) & ~15;
-  const int KB = a.kb, ns = (KB + KS - 1) / KS;
+  // this CTA's blocks of k
+  const int kb0 = (int)((long long)a.kb * rank / a.split), kb1 = (int)((long long)a.kb * (rank + 1) / a.split);
+  const int ns = (kb1 - kb0 + KS - 1) / KS;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&sfull[s], 1);
-      mbar_init(&sempty[s], QL_EPI_WARPS);
+      mbar_init(&sempty[s], Cfg::ALT ? 4 : QL_EPI_WARPS);
     }
     for (int b = 0; b < NBUF; ++b) {
       mbar_init(&accfull[b], 1);
@@ -137,20 +151,26 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     // --------------------------------------------------------- TMA producer
     // Weight rows past the end and columns of k past the end arrive as zeros.
     bool ok = true;
+    int s = 0;
+    uint32_t ph = 1;
     for (int i = 0; i < ns; ++i) {
-      const int s = i % STAGES, f = i / STAGES;
-      if (f > 0) ok = mbar_wait_warp(&empty[s], (f - 1) & 1, abort_flag, a.status);
+      ok = mbar_wait_warp(&empty[s], ph, abort_flag, a.status);   // the first round passes
       if (!ok) break;
       if (elect_one()) {
         uint8_t* st = smem + (size_t)s * Cfg::STAGE;
-        const int nb = min(KS, KB - i * KS);
+        const int kb = kb0 + i * KS, nb = min(KS, kb1 - kb);
+        const uint32_t bar = smem_u32(&full[s]);
         mbar_expect_tx(&full[s], (uint32_t)(nb * (a.h + a.each) * 128));
         for (int j = 0; j < nb; ++j) {
-          tma_2d<1>(st + j * Cfg::A_BYTES, &mW, smem_u32(&full[s]), (i * KS + j) * 128, m0);
-          tma_2d<1>(st + KS * Cfg::A_BYTES + j * Cfg::B_BYTES, &mX, smem_u32(&full[s]), (i * KS + j) * 128, n0);
+          tma_2d<1>(st + j * Cfg::A_BYTES, &mW, bar, (kb + j) * 128, m0);
+          tma_2d<1>(st + KS * Cfg::A_BYTES + j * Cfg::B_BYTES, &mX, bar, (kb + j) * 128, n0);
         }
       }
       __syncwarp();
+      if (++s == STAGES) {
+        s = 0;
+        ph ^= 1;
+      }
     }
     if (!ok) {   // a CTA must not exit before its copies have landed: wait far longer than they take
       const uint64_t t0 = globaltimer();
@@ -158,56 +178,66 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     }
   } else if (warp == QL_SCALE) {
     // --------------------------------------------- the tokens' scales, by stage
+    constexpr int NC = (BN + 31) / 32;
+    int s = 0;
+    uint32_t ph = 1;
     for (int i = 0; i < ns; ++i) {
-      const int s = i % STAGES, f = i / STAGES;
-      if (f > 0 && !mbar_wait_warp(&sempty[s], (f - 1) & 1, abort_flag, a.status)) break;
-      float v[KS][(BN + 31) / 32];
+      float v[KS][NC];
 #pragma unroll
       for (int j = 0; j < KS; ++j)
 #pragma unroll
-        for (int c = 0; c < (BN + 31) / 32; ++c) {
-          const int kb = i * KS + j, col = c * 32 + lane;
-          v[j][c] = kb < KB && col < cols ? a.xs[(size_t)(n0 + col) * KB + kb] : 0.0f;
+        for (int c = 0; c < NC; ++c) {
+          const int kb = kb0 + i * KS + j, col = c * 32 + lane;
+          v[j][c] = kb < kb1 && col < cols ? a.xs[(size_t)(n0 + col) * a.kb + kb] : 0.0f;
         }
+      if (!mbar_wait_warp(&sempty[s], ph, abort_flag, a.status)) break;
 #pragma unroll
       for (int j = 0; j < KS; ++j)
 #pragma unroll
-        for (int c = 0; c < (BN + 31) / 32; ++c)
+        for (int c = 0; c < NC; ++c)
           if (c * 32 + lane < BN) s_xs[(s * KS + j) * BN + c * 32 + lane] = v[j][c];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sfull[s]);
+      if (++s == STAGES) {
+        s = 0;
+        ph ^= 1;
+      }
     }
   } else if (warp == QL_MMA) {
     // ----------------------------------------------------------- MMA issuer
     const uint32_t idesc = idesc_e4m3_f32(128, bn);
-    bool ok = true;
-    for (int i = 0; i < ns && ok; ++i) {
-      const int s = i % STAGES, f = i / STAGES;
-      ok = mbar_wait_warp(&full[s], f & 1, abort_flag, a.status);
-      if (!ok) break;
-      for (int j = 0; j < KS; ++j) {
-        const int kb = i * KS + j;
-        if (kb >= KB) break;
-        const int b = kb % NBUF;
-        if (kb >= NBUF) ok = mbar_wait_warp(&accfree[b], (kb / NBUF - 1) & 1, abort_flag, a.status);
+    const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
+    if (elect_one()) {
+      bool ok = true;
+      int s = 0, b = 0;
+      uint32_t ph = 0, bph = 1;        // phase of full[s]; of accfree[b] (free in the first round)
+      for (int i = 0; i < ns; ++i) {
+        ok = mbar_wait(&full[s], ph, abort_flag, a.status) && mbar_wait(&accfree[b], bph, abort_flag, a.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + (size_t)s * Cfg::STAGE + j * Cfg::A_BYTES);
-        const uint32_t sb = smem_u32(smem + (size_t)s * Cfg::STAGE + KS * Cfg::A_BYTES + j * Cfg::B_BYTES);
-        const uint64_t ad = sdesc_k_sw128(sa), bd = sdesc_k_sw128(sb);
-        if (elect_one()) {
+        const uint64_t ad = desc0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = ad + KS * (Cfg::A_BYTES / 16);
+        const int nb = min(KS, kb1 - kb0 - i * KS);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            pair_mma<1, true>(tmem + (uint32_t)(b * BN), ad + 2u * k, bd + 2u * k, idesc, k ? 1u : 0u);
-          tc_commit(&accfull[b]);
+        for (int j = 0; j < KS; ++j)
+          if (j < nb) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              pair_mma<1, true>(tmem + (uint32_t)((b * KS + j) * BN), ad + j * (Cfg::A_BYTES / 16) + 2 * k,
+                                bd + j * (Cfg::B_BYTES / 16) + 2 * k, idesc, k ? 1u : 0u);
+          }
+        tc_commit(&accfull[b]);
+        tc_commit(&empty[s]);
+        if (++b == NBUF) {
+          b = 0;
+          bph ^= 1;
         }
-        __syncwarp();
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      if (!ok) break;
-      if (elect_one()) tc_commit(&empty[s]);
-      __syncwarp();
+      tc_commit(mma_done);
     }
-    if (elect_one()) tc_commit(mma_done);
     __syncwarp();
     if (lane == 0) {   // every MMA is complete before TMEM is freed
       const uint64_t t0 = globaltimer();
@@ -225,61 +255,61 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     const int c0 = Cfg::ALT ? 0 : wg * COLS;            // first column of this thread
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const bool in = row < a.h && m < a.n;
-    const float* ws = a.Ws + (size_t)(in ? m / Q_GROUP : 0) * KB;
+    const float* ws = a.Ws + (size_t)(in ? m / Q_GROUP : 0) * a.kb;
     uint64_t acc[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[i] = 0;
-    bool ok = true;
-    float w_next = ws[0];
-    for (int i = 0; i < ns && ok; ++i) {
-      const int s = i % STAGES, f = i / STAGES;
-      ok = mbar_wait_warp(&sfull[s], f & 1, abort_flag, a.status);
-      for (int j = 0; j < KS && ok; ++j) {
-        const int kb = i * KS + j;
-        if (kb >= KB) break;
-        const float w = w_next;
-        if (kb + 1 < KB) w_next = ws[kb + 1];
-        if (Cfg::ALT && (kb & 1) != wg) continue;
-        const int b = kb % NBUF;
-        ok = mbar_wait_warp(&accfull[b], (kb / NBUF) & 1, abort_flag, a.status);
-        if (!ok) break;
-        tc_fence_after();
-        const float4* xs = reinterpret_cast<const float4*>(s_xs + (s * KS + j) * BN + c0);
-        const uint64_t w2 = pack2(w, w);
+    for (int i = Cfg::ALT ? wg : 0; i < ns; i += Cfg::ALT ? 2 : 1) {
+      const int s = i % STAGES, b = i % NBUF, kb = kb0 + i * KS;
+      float w[KS];
 #pragma unroll
-        for (int c = 0; c < COLS; c += 16) {
-          if (c0 + c < cols) {
-            float v[16];
-            tmem_ld16(tlane + (uint32_t)(b * BN + c0 + c), v);
+      for (int j = 0; j < KS; ++j) w[j] = kb + j < kb1 ? ws[kb + j] : 0.0f;
+      if (!mbar_wait_warp(&sfull[s], (i / STAGES) & 1, abort_flag, a.status) ||
+          !mbar_wait_warp(&accfull[b], (i / NBUF) & 1, abort_flag, a.status))
+        break;
+      tc_fence_after();
 #pragma unroll
-            for (int u = 0; u < 16; u += 4) {
-              const float4 x = xs[(c + u) / 4];
-              acc[(c + u) / 2] = fma2(pack2(v[u], v[u + 1]), mul2(pack2(x.x, x.y), w2), acc[(c + u) / 2]);
-              acc[(c + u) / 2 + 1] = fma2(pack2(v[u + 2], v[u + 3]), mul2(pack2(x.z, x.w), w2), acc[(c + u) / 2 + 1]);
+      for (int j = 0; j < KS; ++j) {
+        if (kb + j < kb1) {
+          const float4* xs = reinterpret_cast<const float4*>(s_xs + (s * KS + j) * BN + c0);
+          const uint64_t w2 = pack2(w[j], w[j]);
+#pragma unroll
+          for (int c = 0; c < COLS; c += 16) {
+            if (c0 + c < cols) {
+              float v[16];
+              tmem_ld16(tlane + (uint32_t)((b * KS + j) * BN + c0 + c), v);
+#pragma unroll
+              for (int u = 0; u < 16; u += 4) {
+                const float4 x = xs[(c + u) / 4];
+                acc[(c + u) / 2] = fma2(pack2(v[u], v[u + 1]), mul2(pack2(x.x, x.y), w2), acc[(c + u) / 2]);
+                acc[(c + u) / 2 + 1] = fma2(pack2(v[u + 2], v[u + 3]), mul2(pack2(x.z, x.w), w2), acc[(c + u) / 2 + 1]);
+              }
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&accfree[b]);
       }
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sempty[s]);
+      if (lane == 0) {
+        mbar_arrive(&accfree[b]);
+        mbar_arrive(&sempty[s]);
+      }
     }
-    if (Cfg::ALT) {
-      // The odd blocks' sums join the even blocks', through the ring's memory:
-      // once both warpgroups have seen their last block, every copy and MMA of
-      // this CTA has completed.
+    float* ex = reinterpret_cast<float*>(smem);       // [BN][128], in the ring's memory (see below)
+    if (Cfg::ALT || a.split > 1) {
+      // Once both warpgroups have seen their last stage, every copy and MMA of
+      // this CTA has completed and the ring is free.
       named_bar_sync(1, QL_EPI_WARPS * 32);
-      float* ex = reinterpret_cast<float*>(smem);       // [COLS][128]
       if (wg == 1)
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           float u, v;
           unpack2(acc[i], u, v);
-          ex[(2 * i) * 128 + row] = u;
-          ex[(2 * i + 1) * 128 + row] = v;
+          ex[(c0 + 2 * i) * 128 + row] = u;
+          ex[(c0 + 2 * i + 1) * 128 + row] = v;
         }
+    }
+    if (Cfg::ALT) {   // the odd stages' sums join the even stages'
       named_bar_sync(1, QL_EPI_WARPS * 32);
       if (wg == 0)
 #pragma unroll
@@ -289,19 +319,252 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
           acc[i] = pack2(u + ex[(2 * i) * 128 + row], v + ex[(2 * i + 1) * 128 + row]);
         }
     }
-    if (in && !*abort_flag && !(Cfg::ALT && wg == 1)) {
+    if (a.split > 1) {
+      if (wg == 0)
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          float u, v;
+          unpack2(acc[i], u, v);
+          ex[(c0 + 2 * i) * 128 + row] = u;
+          ex[(c0 + 2 * i + 1) * 128 + row] = v;
+        }
+    } else if (in && !*abort_flag && !(Cfg::ALT && wg == 1)) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         float u, v;
         unpack2(acc[i], u, v);
         const int c = c0 + 2 * i;
         const size_t at = (size_t)(n0 + c) * a.n + m;
-        if (a.y_f32) {
-          if (c < cols) reinterpret_cast<float*>(a.y)[at] = u;
-          if (c + 1 < cols) reinterpret_cast<float*>(a.y)[at + a.n] = v;
-        } else {
-          if (c < cols) reinterpret_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16(u);
-          if (c + 1 < cols) reinterpret_cast<__nv_bfloat16*>(a.y)[at + a.n] = __float2bfloat16(v);
+        if (c < cols) put_y(a.y, a.y_f32, at, u);
+        if (c + 1 < cols) put_y(a.y, a.y_f32, at + a.n, v);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (a.split > 1) {
+    cluster_sync();   // every CTA's sums are in its ex
+    // CTA `rank` adds up and stores every split-th column
+    const int row = threadIdx.x & 127, m = m0 + row;
+    if (threadIdx.x < QL_EPI_WARPS * 32 && row < a.h && m < a.n && !*abort_flag) {
+      const uint32_t ex = smem_u32(smem);
+      for (int c = rank + a.split * (threadIdx.x >> 7); c < cols; c += 2 * a.split) {
+        float v = 0.0f;
+        for (int r = 0; r < a.split; ++r) {
+          float u;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                       : "=f"(u)
+                       : "r"(cluster_addr(ex + (uint32_t)(c * 128 + row) * 4, (uint32_t)r))
+                       : "memory");
+          v += u;
+        }
+        put_y(a.y, a.y_f32, (size_t)(n0 + c) * a.n + m, v);
+      }
+    }
+    __syncwarp();
+    cluster_sync();   // nobody leaves while its sums are read
+  }
+  __syncthreads();
+  if (warp == QL_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, NCOLS);
+  }
+}
+
+// ---------------------------------------------------------------- many tokens
+constexpr int QR_THREADS = (QL_EPI_WARPS + 2) * 32;
+template <int CTAS>
+struct QrCfg {
+  static constexpr int BN = 256;                        // weight rows per tile, at most
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / CTAS * 128;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int FIXED = 1024 + 256;
+  static constexpr int STAGES = (QL_SMEM - FIXED) / STAGE;
+  static constexpr int SMEM = FIXED + STAGES * STAGE;
+};
+
+// Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (a multiple of 32).
+template <int CTAS>
+__global__ void __launch_bounds__(QR_THREADS, 1)
+k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW, const QlinArgs a) {
+  using Cfg = QrCfg<CTAS>;
+  constexpr int STAGES = Cfg::STAGES, BN = Cfg::BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * Cfg::STAGE);
+  uint64_t* empty = full + STAGES;
+  uint64_t* accfull = empty + STAGES;   // [2]
+  uint64_t* accfree = accfull + 2;      // [2]
+  uint64_t* mma_done = accfree + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((2 * STAGES + 5) * 8 + 8 <= 256, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
+  const int mt = (a.T + 128 * CTAS - 1) / (128 * CTAS), n_tiles = mt * ((a.n + a.each - 1) / a.each);
+  const int KB = a.kb, half = a.each / CTAS;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], CTAS);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accfree[b], QL_EPI_WARPS * CTAS);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == QL_MMA) pair_tmem_alloc<CTAS>(tmem_slot, 512);
+  if (warp == QL_PRODUCER && lane == 0) {
+    tma_prefetch_desc(&mX);
+    tma_prefetch_desc(&mW);
+  }
+  tc_fence_before();
+  if (CTAS == 2) cluster_sync();   // the barriers of both CTAs are ready
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();   // operands and outputs belong to the stream order
+
+  if (warp == QL_PRODUCER) {
+    // --------------------------------------------------------- TMA producer
+    bool ok = true;
+    int s = 0;
+    uint32_t ph = 1;
+    for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
+      const int m0 = (w % mt * CTAS + (int)rank) * 128, n0 = w / mt * a.each + (int)rank * half;
+      for (int kb = 0; kb < KB; ++kb) {
+        ok = mbar_wait_warp(&empty[s], ph, abort_flag, a.status);   // the first round passes
+        if (!ok) break;
+        if (elect_one()) {
+          uint8_t* st = smem + (size_t)s * Cfg::STAGE;
+          const uint32_t bytes = (uint32_t)(128 + half) * 128;
+          const uint32_t bar = CTAS == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+          if (CTAS == 2) mbar_expect_cluster(bar, bytes);
+          else mbar_expect_tx(&full[s], bytes);
+          tma_2d<CTAS>(st, &mX, bar, kb * 128, m0);
+          tma_2d<CTAS>(st + Cfg::A_BYTES, &mW, bar, kb * 128, n0);
+        }
+        __syncwarp();
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok) {   // a CTA must not exit before its copies have landed: wait far longer than they take
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
+    }
+  } else if (warp == QL_MMA) {
+    // ----------------------------------------------------------- MMA issuer
+    // One thread (of the pair's first CTA).  An MMA's issue waits for the one
+    // before it, so the next block's barriers are looked at between this
+    // block's MMAs: a wait after them would leave the tensor core idle.
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_e4m3_f32(128 * CTAS, a.each);
+      const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
+      bool ok = true, there = false, free = true;
+      int s = 0, b = 0;
+      uint32_t ph = 0, bph = 1;        // phase of full[s]; of accfree[b] (free in the first round)
+      for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!there) ok = mbar_wait(&full[s], ph, abort_flag, a.status);
+          if (ok && !free) ok = mbar_wait(&accfree[b], bph, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ad = desc0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = ad + Cfg::A_BYTES / 16;
+          const uint32_t d = tmem + (uint32_t)(b * BN);
+          uint64_t *const done = &accfull[b], *const used = &empty[s];
+          pair_mma<CTAS, true>(d, ad, bd, idesc, 0u);
+          pair_mma<CTAS, true>(d, ad + 2, bd + 2, idesc, 1u);
+          pair_mma<CTAS, true>(d, ad + 4, bd + 4, idesc, 1u);
+          b ^= 1;
+          if (!b) bph ^= 1;
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+          there = mbar_try_wait(&full[s], ph);
+          free = mbar_try_wait(&accfree[b], bph);
+          pair_mma<CTAS, true>(d, ad + 6, bd + 6, idesc, 1u);
+          pair_commit<CTAS>(done);
+          pair_commit<CTAS>(used);
+        }
+      }
+      pair_commit<CTAS>(mma_done);
+    }
+  } else {
+    // ------------------------------------------------------------- epilogue
+    // A thread has one token and half of the tile's columns, at most 128; they
+    // touch two weight blocks at most, the second from column `edge` on.
+    const int wg = warp >> 2, hc = a.each / 2;
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(wg * hc);
+    const uint32_t free0 = CTAS == 2 ? cluster_addr(smem_u32(&accfree[0]), 0) : smem_u32(&accfree[0]);
+    const int nblk = (a.n + Q_GROUP - 1) / Q_GROUP;
+    int b = 0;
+    uint32_t bph = 0;
+    bool ok = true;
+    for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
+      const int t = (w % mt * CTAS + (int)rank) * 128 + (warp & 3) * 32 + lane;
+      const int n0 = w / mt * a.each + wg * hc;
+      const int edge = Q_GROUP - (n0 & (Q_GROUP - 1));
+      const float* xs = a.xs + (size_t)min(t, a.T - 1) * KB;
+      const float* w0 = a.Ws + (size_t)min(n0 / Q_GROUP, nblk - 1) * KB;
+      const float* w1 = a.Ws + (size_t)min(n0 / Q_GROUP + 1, nblk - 1) * KB;
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      float x_n = xs[0], u_n = w0[0], v_n = w1[0];
+      for (int kb = 0; kb < KB; ++kb) {
+        const float su = x_n * u_n, sv = x_n * v_n;
+        const int kn = min(kb + 1, KB - 1);
+        x_n = xs[kn];
+        u_n = w0[kn];
+        v_n = w1[kn];
+        ok = mbar_wait_warp(&accfull[b], bph, abort_flag, a.status);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          if (c < hc) {
+            float v[32];
+            tmem_ld32(tlane + (uint32_t)(b * BN + c), v);
+#pragma unroll
+            for (int q = 0; q < 32; q += 16) {
+              const float sc = c + q < edge ? su : sv;
+              const uint64_t s2 = pack2(sc, sc);
+#pragma unroll
+              for (int i = q; i < q + 16; i += 2) acc[(c + i) / 2] = fma2(pack2(v[i], v[i + 1]), s2, acc[(c + i) / 2]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CTAS == 2) mbar_arrive_cluster(free0 + 8 * b);
+          else mbar_arrive(&accfree[b]);
+        }
+        b ^= 1;
+        if (!b) bph ^= 1;
+      }
+      if (!ok) break;
+      const int cols = min(hc, a.n - n0);   // a multiple of 8
+      if (t < a.T) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          if (c < cols) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack2(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
+            const size_t at = ((size_t)t * a.n + n0 + c) / 8;
+            if (a.y_f32) store8_f32(a.y, at, v);
+            else store8_bf16(a.y, at, v);
+          }
         }
       }
     }
@@ -309,9 +572,13 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  // every MMA of the pair is complete before TMEM is freed
+  if (warp == QL_MMA) mbar_wait_warp(mma_done, 0, abort_flag, a.status);
+  __syncwarp();
+  if (CTAS == 2) cluster_sync();   // neither CTA leaves while the other may still signal or read it
   if (warp == QL_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, NCOLS);
+    pair_tmem_dealloc<CTAS>(tmem, 512);
   }
 }
 
