@@ -372,20 +372,21 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 }
 
 // ---------------------------------------------------------------- many tokens
-constexpr int QR_THREADS = (QL_EPI_WARPS + 2) * 32;
+constexpr int QR_SLOT = 132;    // floats of one block's scales: 128 tokens, up to 3 weight blocks
+
 template <int CTAS>
 struct QrCfg {
   static constexpr int BN = 256;                        // weight rows per tile, at most
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / CTAS * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int FIXED = 1024 + 256;
+  static constexpr int FIXED = 1024 + 256 + 2 * QR_SLOT * 4;
   static constexpr int STAGES = (QL_SMEM - FIXED) / STAGE;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
 };
 
 // Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (a multiple of 32).
 template <int CTAS>
-__global__ void __launch_bounds__(QR_THREADS, 1)
+__global__ void __launch_bounds__(QL_THREADS, 1)
 k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW, const QlinArgs a) {
   using Cfg = QrCfg<CTAS>;
   constexpr int STAGES = Cfg::STAGES, BN = Cfg::BN;
@@ -395,10 +396,12 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
   uint64_t* empty = full + STAGES;
   uint64_t* accfull = empty + STAGES;   // [2]
   uint64_t* accfree = accfull + 2;      // [2]
-  uint64_t* mma_done = accfree + 2;
+  uint64_t* sfree = accfree + 2;        // [2] this CTA's epilogue is done with a slot of scales
+  uint64_t* mma_done = sfree + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * STAGES + 5) * 8 + 8 <= 256, "barrier area");
+  float* slots = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE + 256);   // [2][QR_SLOT]
+  static_assert((2 * STAGES + 7) * 8 + 8 <= 256, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
@@ -411,8 +414,9 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&accfull[b], 1);
+      mbar_init(&accfull[b], 2);        // the MMAs' sums, and their scales
       mbar_init(&accfree[b], QL_EPI_WARPS * CTAS);
+      mbar_init(&sfree[b], QL_EPI_WARPS);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -460,6 +464,54 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
       const uint64_t t0 = globaltimer();
       while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
     }
+  } else if (warp == QL_SCALE) {
+    // -------------------------------------------- scales, a block ahead of use
+    // The next four blocks' values are in flight while this block's are written.
+    int b = 0;
+    uint32_t bph = 1;
+    bool ok = true;
+    for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
+      const int m0 = (w % mt * CTAS + (int)rank) * 128, nb0 = w / mt * a.each / Q_GROUP;
+      const int nblk = (a.n + Q_GROUP - 1) / Q_GROUP;
+      const float* x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = a.xs + (size_t)min(m0 + i * 32 + lane, a.T - 1) * KB;
+      const float* ws = a.Ws + (size_t)min(nb0 + min(lane, 2), nblk - 1) * KB;
+      float v[4][5], n[4][5];
+      auto fetch = [&](int kb, float (&f)[4][5]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = min(kb + j, KB - 1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[j][i] = x[i][k];
+          f[j][4] = ws[k];
+        }
+      };
+      fetch(0, n);
+      for (int kb = 0; kb < KB && ok; kb += 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 5; ++i) v[j][i] = n[j][i];
+        if (kb + 4 < KB) fetch(kb + 4, n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (kb + j < KB && ok) {
+            ok = mbar_wait_warp(&sfree[b], bph, abort_flag, a.status);   // the first round passes
+            if (ok) {
+              float* slot = slots + b * QR_SLOT;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) slot[i * 32 + lane] = v[j][i];
+              if (lane < 3) slot[128 + lane] = v[j][4];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&accfull[b]);
+              b ^= 1;
+              if (!b) bph ^= 1;
+            }
+          }
+        }
+      }
+    }
   } else if (warp == QL_MMA) {
     // ----------------------------------------------------------- MMA issuer
     // One thread (of the pair's first CTA).  An MMA's issue waits for the one
@@ -505,7 +557,6 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     const int wg = warp >> 2, hc = a.each / 2;
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(wg * hc);
     const uint32_t free0 = CTAS == 2 ? cluster_addr(smem_u32(&accfree[0]), 0) : smem_u32(&accfree[0]);
-    const int nblk = (a.n + Q_GROUP - 1) / Q_GROUP;
     int b = 0;
     uint32_t bph = 0;
     bool ok = true;
@@ -513,21 +564,16 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
       const int t = (w % mt * CTAS + (int)rank) * 128 + (warp & 3) * 32 + lane;
       const int n0 = w / mt * a.each + wg * hc;
       const int edge = Q_GROUP - (n0 & (Q_GROUP - 1));
-      const float* xs = a.xs + (size_t)min(t, a.T - 1) * KB;
-      const float* w0 = a.Ws + (size_t)min(n0 / Q_GROUP, nblk - 1) * KB;
-      const float* w1 = a.Ws + (size_t)min(n0 / Q_GROUP + 1, nblk - 1) * KB;
+      const int blk = n0 / Q_GROUP - w / mt * a.each / Q_GROUP;   // this half's first block, within the tile
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float x_n = xs[0], u_n = w0[0], v_n = w1[0];
       for (int kb = 0; kb < KB; ++kb) {
-        const float su = x_n * u_n, sv = x_n * v_n;
-        const int kn = min(kb + 1, KB - 1);
-        x_n = xs[kn];
-        u_n = w0[kn];
-        v_n = w1[kn];
         ok = mbar_wait_warp(&accfull[b], bph, abort_flag, a.status);
         if (!ok) break;
+        const float* slot = slots + b * QR_SLOT;
+        const float x = slot[(warp & 3) * 32 + lane];
+        const float su = x * slot[128 + blk], sv = x * slot[128 + min(blk + 1, 2)];
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
@@ -548,6 +594,7 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
         if (lane == 0) {
           if (CTAS == 2) mbar_arrive_cluster(free0 + 8 * b);
           else mbar_arrive(&accfree[b]);
+          mbar_arrive(&sfree[b]);
         }
         b ^= 1;
         if (!b) bph ^= 1;
