@@ -338,18 +338,19 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         ok = mbar_wait_warp(&accfull[b], (uint32_t)((ci >> 1) & 1), abort_flag, args.status);
         if (!ok) break;
         tc_fence_after();
+        // all of the tile's columns, computed or not: what the others hold is
+        // never stored, and a test would cost a select per value
+        const uint32_t at = tlane + (uint32_t)(b * BN + (BN >= 64 ? 32 * wg : 0));
+        if (kc == 0) {
 #pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-          const int c = 64 * j + 32 * wg;
-          if (c < t.cols) {
-            if (kc == 0) {
-              tmem_ld32(tlane + (uint32_t)(b * BN + c), acc[j]);
-            } else {
-              float v[32];
-              tmem_ld32(tlane + (uint32_t)(b * BN + c), v);
+          for (int j = 0; j < NCH; ++j) tmem_get32(at + 64u * j, acc[j]);
+        } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) acc[j][i] += v[i];
-            }
+          for (int j = 0; j < NCH; ++j) {
+            float v[32];
+            tmem_get32(at + 64u * j, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[j][i] += v[i];
           }
         }
         tc_fence_before();

@@ -308,7 +308,7 @@ sffn_status qlinear_rows(const sffn_qlinear_handle* h, const void* xq, QlinArgs 
   if (tiles > 0x7FFFFFFFll) return SFFN_ERR_UNSUPPORTED;
   CUtensorMap mX, mW;
   if (!code_map(&mX, xq, a.k, a.T, 128) || !code_map(&mW, h->desc.Wq, a.k, a.n, a.each / CTAS)) return SFFN_ERR_CUDA;
-  return launched(launch_pdl(k_qlinear_rows<CTAS>, dim3((unsigned)std::min(tiles, slots) * CTAS), dim3(QL_THREADS),
+  return launched(launch_pdl(k_qlinear_rows<CTAS>, dim3((unsigned)std::min(tiles, slots) * CTAS), dim3(QR_THREADS),
                              (size_t)QrCfg<CTAS>::SMEM, st, CTAS, mX, mW, a));
 }
 

@@ -35,26 +35,6 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Two fp32 lanes at a time.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 struct QlinArgs {
   const float* xs;      // [T][kb]
   const float* Ws;      // [ceil(n/128)][kb]
@@ -250,15 +230,15 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     }
   } else {
     // ------------------------------------------------------------- epilogue
-    constexpr int COLS = Cfg::COLS, P = COLS / 2;
+    constexpr int COLS = Cfg::COLS;
     const int wg = warp >> 2, row = (warp & 3) * 32 + lane, m = m0 + row;
     const int c0 = Cfg::ALT ? 0 : wg * COLS;            // first column of this thread
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const bool in = row < a.h && m < a.n;
     const float* ws = a.Ws + (size_t)(in ? m / Q_GROUP : 0) * a.kb;
-    uint64_t acc[P];
+    float acc[COLS];
 #pragma unroll
-    for (int i = 0; i < P; ++i) acc[i] = 0;
+    for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
     for (int i = Cfg::ALT ? wg : 0; i < ns; i += Cfg::ALT ? 2 : 1) {
       const int s = i % STAGES, b = i % NBUF, kb = kb0 + i * KS;
       float w[KS];
@@ -272,18 +252,17 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       for (int j = 0; j < KS; ++j) {
         if (kb + j < kb1) {
           const float4* xs = reinterpret_cast<const float4*>(s_xs + (s * KS + j) * BN + c0);
-          const uint64_t w2 = pack2(w[j], w[j]);
 #pragma unroll
           for (int c = 0; c < COLS; c += 16) {
-            if (c0 + c < cols) {
-              float v[16];
-              tmem_ld16(tlane + (uint32_t)((b * KS + j) * BN + c0 + c), v);
+            float v[16];
+            tmem_get16(tlane + (uint32_t)((b * KS + j) * BN + c0 + c), v);
 #pragma unroll
-              for (int u = 0; u < 16; u += 4) {
-                const float4 x = xs[(c + u) / 4];
-                acc[(c + u) / 2] = fma2(pack2(v[u], v[u + 1]), mul2(pack2(x.x, x.y), w2), acc[(c + u) / 2]);
-                acc[(c + u) / 2 + 1] = fma2(pack2(v[u + 2], v[u + 3]), mul2(pack2(x.z, x.w), w2), acc[(c + u) / 2 + 1]);
-              }
+            for (int u = 0; u < 16; u += 4) {
+              const float4 x = xs[(c + u) / 4];
+              acc[c + u] = fmaf(v[u], x.x * w[j], acc[c + u]);
+              acc[c + u + 1] = fmaf(v[u + 1], x.y * w[j], acc[c + u + 1]);
+              acc[c + u + 2] = fmaf(v[u + 2], x.z * w[j], acc[c + u + 2]);
+              acc[c + u + 3] = fmaf(v[u + 3], x.w * w[j], acc[c + u + 3]);
             }
           }
         }
@@ -302,42 +281,22 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       named_bar_sync(1, QL_EPI_WARPS * 32);
       if (wg == 1)
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          float u, v;
-          unpack2(acc[i], u, v);
-          ex[(c0 + 2 * i) * 128 + row] = u;
-          ex[(c0 + 2 * i + 1) * 128 + row] = v;
-        }
+        for (int i = 0; i < COLS; ++i) ex[(c0 + i) * 128 + row] = acc[i];
     }
     if (Cfg::ALT) {   // the odd stages' sums join the even stages'
       named_bar_sync(1, QL_EPI_WARPS * 32);
       if (wg == 0)
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          float u, v;
-          unpack2(acc[i], u, v);
-          acc[i] = pack2(u + ex[(2 * i) * 128 + row], v + ex[(2 * i + 1) * 128 + row]);
-        }
+        for (int i = 0; i < COLS; ++i) acc[i] += ex[i * 128 + row];
     }
     if (a.split > 1) {
       if (wg == 0)
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          float u, v;
-          unpack2(acc[i], u, v);
-          ex[(c0 + 2 * i) * 128 + row] = u;
-          ex[(c0 + 2 * i + 1) * 128 + row] = v;
-        }
+        for (int i = 0; i < COLS; ++i) ex[(c0 + i) * 128 + row] = acc[i];
     } else if (in && !*abort_flag && !(Cfg::ALT && wg == 1)) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        float u, v;
-        unpack2(acc[i], u, v);
-        const int c = c0 + 2 * i;
-        const size_t at = (size_t)(n0 + c) * a.n + m;
-        if (c < cols) put_y(a.y, a.y_f32, at, u);
-        if (c + 1 < cols) put_y(a.y, a.y_f32, at + a.n, v);
-      }
+      for (int i = 0; i < COLS; ++i)
+        if (c0 + i < cols) put_y(a.y, a.y_f32, (size_t)(n0 + c0 + i) * a.n + m, acc[i]);
     }
   }
   __syncwarp();
@@ -372,6 +331,11 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 }
 
 // ---------------------------------------------------------------- many tokens
+// Sixteen epilogue warps: a block's sums have to leave TMEM and be scaled in the
+// time of four MMAs, and every step of that (wait, load, signal) is latency.
+constexpr int QR_EPI_WARPS = 16;
+constexpr int QR_PRODUCER = QR_EPI_WARPS, QR_MMA = QR_EPI_WARPS + 1, QR_SCALE = QR_EPI_WARPS + 2;
+constexpr int QR_THREADS = (QR_EPI_WARPS + 3) * 32;
 constexpr int QR_SLOT = 132;    // floats of one block's scales: 128 tokens, up to 3 weight blocks
 
 template <int CTAS>
@@ -386,7 +350,7 @@ struct QrCfg {
 
 // Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (a multiple of 32).
 template <int CTAS>
-__global__ void __launch_bounds__(QL_THREADS, 1)
+__global__ void __launch_bounds__(QR_THREADS, 1)
 k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW, const QlinArgs a) {
   using Cfg = QrCfg<CTAS>;
   constexpr int STAGES = Cfg::STAGES, BN = Cfg::BN;
@@ -415,15 +379,15 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 2);        // the MMAs' sums, and their scales
-      mbar_init(&accfree[b], QL_EPI_WARPS * CTAS);
-      mbar_init(&sfree[b], QL_EPI_WARPS);
+      mbar_init(&accfree[b], QR_EPI_WARPS * CTAS);
+      mbar_init(&sfree[b], QR_EPI_WARPS);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == QL_MMA) pair_tmem_alloc<CTAS>(tmem_slot, 512);
-  if (warp == QL_PRODUCER && lane == 0) {
+  if (warp == QR_MMA) pair_tmem_alloc<CTAS>(tmem_slot, 512);
+  if (warp == QR_PRODUCER && lane == 0) {
     tma_prefetch_desc(&mX);
     tma_prefetch_desc(&mW);
   }
@@ -434,7 +398,7 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
   const uint32_t tmem = *tmem_slot;
   griddep_wait();   // operands and outputs belong to the stream order
 
-  if (warp == QL_PRODUCER) {
+  if (warp == QR_PRODUCER) {
     // --------------------------------------------------------- TMA producer
     bool ok = true;
     int s = 0;
@@ -464,7 +428,7 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
       const uint64_t t0 = globaltimer();
       while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
     }
-  } else if (warp == QL_SCALE) {
+  } else if (warp == QR_SCALE) {
     // -------------------------------------------- scales, a block ahead of use
     // The next four blocks' values are in flight while this block's are written.
     int b = 0;
@@ -512,7 +476,7 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
         }
       }
     }
-  } else if (warp == QL_MMA) {
+  } else if (warp == QR_MMA) {
     // ----------------------------------------------------------- MMA issuer
     // One thread (of the pair's first CTA).  An MMA's issue waits for the one
     // before it, so the next block's barriers are looked at between this
@@ -541,8 +505,8 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
             s = 0;
             ph ^= 1;
           }
-          there = mbar_try_wait(&full[s], ph);
-          free = mbar_try_wait(&accfree[b], bph);
+          there = mbar_test(&full[s], ph);
+          free = mbar_test(&accfree[b], bph);
           pair_mma<CTAS, true>(d, ad + 6, bd + 6, idesc, 1u);
           pair_commit<CTAS>(done);
           pair_commit<CTAS>(used);
@@ -552,42 +516,40 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     }
   } else {
     // ------------------------------------------------------------- epilogue
-    // A thread has one token and half of the tile's columns, at most 128; they
-    // touch two weight blocks at most, the second from column `edge` on.
-    const int wg = warp >> 2, hc = a.each / 2;
-    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(wg * hc);
+    // A thread has one token and every fourth 16 columns of the tile: at most
+    // 64.  The tile touches up to three weight blocks.
+    const int wg = warp >> 2;
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t free0 = CTAS == 2 ? cluster_addr(smem_u32(&accfree[0]), 0) : smem_u32(&accfree[0]);
     int b = 0;
     uint32_t bph = 0;
     bool ok = true;
     for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
       const int t = (w % mt * CTAS + (int)rank) * 128 + (warp & 3) * 32 + lane;
-      const int n0 = w / mt * a.each + wg * hc;
-      const int edge = Q_GROUP - (n0 & (Q_GROUP - 1));
-      const int blk = n0 / Q_GROUP - w / mt * a.each / Q_GROUP;   // this half's first block, within the tile
-      uint64_t acc[64];
+      const int n0 = w / mt * a.each;
+      const int edge = Q_GROUP - (n0 & (Q_GROUP - 1));   // first column of the second block
+      float acc[4][16];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[p][i] = 0.0f;
       for (int kb = 0; kb < KB; ++kb) {
         ok = mbar_wait_warp(&accfull[b], bph, abort_flag, a.status);
         if (!ok) break;
+        tc_fence_after();
         const float* slot = slots + b * QR_SLOT;
         const float x = slot[(warp & 3) * 32 + lane];
-        const float su = x * slot[128 + blk], sv = x * slot[128 + min(blk + 1, 2)];
-        tc_fence_after();
+        const float s0 = x * slot[128], s1 = x * slot[129], s2 = x * slot[130];
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          if (c < hc) {
-            float v[32];
-            tmem_ld32(tlane + (uint32_t)(b * BN + c), v);
+        for (int p = 0; p < 4; ++p) {
+          // without a test for narrower tiles: what their unused columns hold is
+          // never stored, and a test would cost a select per sum
+          const int c = 64 * p + 16 * wg;
+          float v[16];
+          tmem_get16(tlane + (uint32_t)(b * BN + c), v);
+          const float sc = c < edge ? s0 : c < edge + Q_GROUP ? s1 : s2;
 #pragma unroll
-            for (int q = 0; q < 32; q += 16) {
-              const float sc = c + q < edge ? su : sv;
-              const uint64_t s2 = pack2(sc, sc);
-#pragma unroll
-              for (int i = q; i < q + 16; i += 2) acc[(c + i) / 2] = fma2(pack2(v[i], v[i + 1]), s2, acc[(c + i) / 2]);
-            }
-          }
+          for (int i = 0; i < 16; ++i) acc[p][i] = fmaf(v[i], sc, acc[p][i]);
         }
         tc_fence_before();
         __syncwarp();
@@ -600,17 +562,20 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
         if (!b) bph ^= 1;
       }
       if (!ok) break;
-      const int cols = min(hc, a.n - n0);   // a multiple of 8
       if (t < a.T) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          if (c < cols) {
-            float v[8];
+        for (int p = 0; p < 4; ++p) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) unpack2(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
-            const size_t at = ((size_t)t * a.n + n0 + c) / 8;
-            if (a.y_f32) store8_f32(a.y, at, v);
-            else store8_bf16(a.y, at, v);
+          for (int i = 0; i < 16; i += 8) {
+            const int c = 64 * p + 16 * wg + i;
+            if (c < a.each && n0 + c < a.n) {   // both multiples of 8
+              float v[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = acc[p][i + j];
+              const size_t at = ((size_t)t * a.n + n0 + c) / 8;
+              if (a.y_f32) store8_f32(a.y, at, v);
+              else store8_bf16(a.y, at, v);
+            }
           }
         }
       }
@@ -620,10 +585,10 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
   tc_fence_before();
   __syncthreads();
   // every MMA of the pair is complete before TMEM is freed
-  if (warp == QL_MMA) mbar_wait_warp(mma_done, 0, abort_flag, a.status);
+  if (warp == QR_MMA) mbar_wait_warp(mma_done, 0, abort_flag, a.status);
   __syncwarp();
   if (CTAS == 2) cluster_sync();   // neither CTA leaves while the other may still signal or read it
-  if (warp == QL_MMA) {
+  if (warp == QR_MMA) {
     tc_fence_after();
     pair_tmem_dealloc<CTAS>(tmem, 512);
   }
