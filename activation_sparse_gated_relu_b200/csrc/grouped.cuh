@@ -32,9 +32,10 @@ namespace sffn {
 enum { GROUPED_FWD = 0, GROUPED_DX = 1, GROUPED_DW = 2 };
 constexpr int GROUPED_MAX_E = 1024;
 constexpr int GT_EPI_WARPS = 8;                        // two warpgroups, every other 32 columns each
-constexpr int GT_PRODUCER = GT_EPI_WARPS, GT_MMA = GT_EPI_WARPS + 1;
-constexpr int GT_FIX = GT_EPI_WARPS + 2;              // clears what lies behind a group's end (weight gradient)
-constexpr int GT_THREADS = (GT_EPI_WARPS + 3) * 32;
+constexpr int GT_PRODUCER = GT_EPI_WARPS;
+constexpr int GT_FIX = GT_EPI_WARPS + 1;              // clears what lies behind a group's end (weight gradient)
+constexpr int GT_MMA = GT_EPI_WARPS + 2;              // and the warp after it: half of a tile's columns each
+constexpr int GT_THREADS = (GT_EPI_WARPS + 4) * 32;
 constexpr int GT_BK = 64;                              // bf16 values of k per stage
 constexpr int GT_SMEM = 227 * 1024;
 
@@ -44,6 +45,9 @@ struct GtCfg {
   static constexpr int B_ROWS = BN / CTAS;             // columns whose operand a CTA holds
   static constexpr int A_BYTES = 128 * GT_BK * 2;
   static constexpr int B_BYTES = B_ROWS * GT_BK * 2;
+  // A CTA's columns of a tile's two halves lie HALF_OFF bytes apart, in boxes of BOX.
+  static constexpr int BOX = BN >= 128 ? 64 : 32;
+  static constexpr int HALF_OFF = B_BYTES / 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int TABLE = (3 * (GROUPED_MAX_E + 1) * 4 + 127) & ~127;
   static constexpr int FIXED = 1024 /*align*/ + 384 /*barriers*/ + TABLE;
@@ -79,6 +83,7 @@ struct GtWalk {
   // the current tile
   int m0;                       // first row m of the tile (of the pair)
   int c0, cols, bn;             // first column, columns stored, columns computed
+  int bn0;                      // of them in the first half (the second may be empty)
   int krow;                     // weight gradient: first row of the group
   int kbs, ktail;               // k blocks, and values in the last one
   size_t orow;                  // output row of column 0
@@ -108,18 +113,20 @@ struct GtWalk {
       orow = (size_t)c0;
     }
     bn = (cols + STEP - 1) / STEP * STEP;
+    bn0 = BN >= 128 ? min(bn, BN / 2) : bn;
   }
 };
 
 template <int MODE, int CTAS, int BN>
 __global__ void __launch_bounds__(GT_THREADS, 1)
 k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
-          const __grid_constant__ CUtensorMap mB32, const GroupedArgs args) {
+          const GroupedArgs args) {
   using Cfg = GtCfg<CTAS, BN>;
   using Walk = GtWalk<MODE, CTAS, BN>;
   constexpr int STAGES = Cfg::STAGES;
   constexpr uint32_t NCOLS = BN <= 16 ? 32 : 2 * BN;     // two accumulators, a power of two of at least 32
   constexpr bool A_MN = MODE != GROUPED_FWD, B_MN = MODE == GROUPED_DW;
+  constexpr int BOX = Cfg::BOX;
   static_assert(NCOLS <= 512 && (NCOLS & (NCOLS - 1)) == 0, "TMEM columns");
   static_assert(!B_MN || Cfg::B_ROWS % 64 == 0, "N-major columns come in boxes of 64");
 
@@ -145,14 +152,14 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], CTAS);        // one arrival per CTA's producer
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);          // both halves' MMAs have read it
       mbar_init(&tailbar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&accfull[b], 1);
+      mbar_init(&accfull[b], 2);
       mbar_init(&accfree[b], GT_EPI_WARPS * CTAS);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -160,7 +167,6 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   if (warp == GT_PRODUCER && lane == 0) {
     tma_prefetch_desc(&mA);
     tma_prefetch_desc(&mB);
-    if (MODE != GROUPED_DW) tma_prefetch_desc(&mB32);
   }
   griddep_wait();   // offsets, operands and outputs belong to the stream order
   for (int e = threadIdx.x; e < args.E; e += GT_THREADS) {
@@ -206,9 +212,12 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
     bool ok = true;
     for (int w = walk0; w < n_tiles && ok; w += n_walk) {
       t.set(w);
-      const int half = t.bn / CTAS, b0 = t.c0 + (int)rank * half, m0 = t.m0 + (int)rank * 128;
-      const int nbox = B_MN ? (half + 63) / 64 : (half + 31) / 32;
-      const uint32_t bytes = Cfg::A_BYTES + nbox * (B_MN ? 8192 : 4096);
+      const int m0 = t.m0 + (int)rank * 128;
+      // this CTA's columns of each half of the tile, boxes of BOX columns
+      const int p0 = t.bn0 / CTAS, p1 = (t.bn - t.bn0) / CTAS;
+      const int b0 = t.c0 + (int)rank * p0, b1 = t.c0 + t.bn0 + (int)rank * p1;
+      const int n0 = (p0 + BOX - 1) / BOX, n1 = (p1 + BOX - 1) / BOX;
+      const uint32_t bytes = Cfg::A_BYTES + (n0 + n1) * (BOX * GT_BK * 2);
       for (int kb = 0; kb < t.kbs; ++kb, ++it) {
         const int s = it % STAGES, f = it / STAGES;
         if (f > 0) ok = mbar_wait_warp(&empty[s], (f - 1) & 1, abort_flag, args.status);
@@ -232,12 +241,11 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
             tma_2d<CTAS>(sa, &mA, bar, m0, t.krow + k0);
             tma_2d<CTAS>(sa + 8192, &mA, bar, m0 + 64, t.krow + k0);
           }
-          if (B_MN) {
-            for (int i = 0; i < nbox; ++i) tma_2d<CTAS>(sb + i * 8192, &mB, bar, b0 + 64 * i, t.krow + k0);
-          } else if (nbox * 32 == Cfg::B_ROWS) {
-            tma_2d<CTAS>(sb, &mB, bar, k0, b0);
-          } else {
-            for (int i = 0; i < nbox; ++i) tma_2d<CTAS>(sb + i * 4096, &mB32, bar, k0, b0 + 32 * i);
+          for (int i = 0; i < n0 + n1; ++i) {
+            const int c = i < n0 ? b0 + BOX * i : b1 + BOX * (i - n0);
+            uint8_t* dst = sb + (i < n0 ? i * (BOX * GT_BK * 2) : Cfg::HALF_OFF + (i - n0) * (BOX * GT_BK * 2));
+            if (B_MN) tma_2d<CTAS>(dst, &mB, bar, c, t.krow + k0);
+            else tma_2d<CTAS>(dst, &mB, bar, k0, c);
           }
         }
       }
@@ -265,7 +273,7 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
       used ^= 1u << s;
       uint8_t* sa = smem + (size_t)s * Cfg::STAGE;
       uint8_t* sb = sa + Cfg::A_BYTES;
-      const int nbox = (t.bn / CTAS + 63) / 64;
+      const int nbox = t.bn > t.bn0 ? 2 : 1;   // the halves, 64 columns each at most
       const int k1 = (t.ktail + 15) & ~15;
       for (int i = lane; i < (k1 - t.ktail) * 8; i += 32) {
         const int at = t.ktail * 128 + i * 16;   // whole rows of 128 bytes: the swizzle permutes within a row
@@ -279,48 +287,55 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         else mbar_arrive(&full[s]);
       }
     }
-  } else if (warp == GT_MMA) {
-    if (rank == 0) {
-      // --------------------------------------------------------- MMA issuer
-      // (of the pair's first CTA)
-      int it = 0, ci = 0;
+  } else if (warp >= GT_MMA) {
+    // ---------------------------------------------------------- MMA issuers
+    // One thread of each of two warps (of the pair's first CTA), a half of the
+    // columns each: an MMA's issue waits for the one before it, so what a
+    // thread does between its MMAs leaves the tensor core idle unless another
+    // thread's are there.
+    const int hf = warp - GT_MMA;
+    if (rank == 0 && elect_one()) {
+      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + Cfg::A_BYTES + hf * Cfg::HALF_OFF;
+      const uint64_t ad0 = A_MN ? sdesc_mn_sw128(sa0, 8192) : sdesc_k_sw128(sa0);
+      const uint64_t bd0 = B_MN ? sdesc_mn_sw128(sb0, 8192) : sdesc_k_sw128(sb0);
+      constexpr uint32_t AK = A_MN ? 128u : 2u, BK = B_MN ? 128u : 2u;   // 16 values of k further
+      int s = 0, b = 0;
+      uint32_t ph = 0, bph = 1;          // phase of full[s]; of accfree[b] (free in the first round)
       bool ok = true;
       for (int w = walk0; w < n_tiles && ok; w += n_walk) {
         t.set(w);
-        const uint32_t idesc = idesc_bf16_f32(128 * CTAS, t.bn) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16);
-        for (int kc = 0; kc < t.kbs && ok; kc += args.kchunk, ++ci) {
-          const int b = ci & 1;
-          if (ci >= 2) ok = mbar_wait_warp(&accfree[b], (uint32_t)(((ci >> 1) - 1) & 1), abort_flag, args.status);
+        const int n = hf ? t.bn - t.bn0 : t.bn0;
+        const uint32_t idesc = idesc_bf16_f32(128 * CTAS, n) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16);
+        for (int kc = 0; kc < t.kbs && ok; kc += args.kchunk) {
+          ok = mbar_wait(&accfree[b], bph, abort_flag, args.status);
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + (uint32_t)(b * BN);
+          const uint32_t d = tmem + (uint32_t)(b * BN) + (hf ? t.bn0 : 0);
           const int k1 = min(kc + args.kchunk, t.kbs);
-          for (int kb = kc; kb < k1; ++kb, ++it) {
-            const int s = it % STAGES, f = it / STAGES;
-            ok = mbar_wait_warp(&full[s], f & 1, abort_flag, args.status);
+          for (int kb = kc; kb < k1; ++kb) {
+            ok = mbar_wait(&full[s], ph, abort_flag, args.status);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sa = smem_u32(smem + (size_t)s * Cfg::STAGE);
-            const uint64_t ad = A_MN ? sdesc_mn_sw128(sa, 8192) : sdesc_k_sw128(sa);
-            const uint64_t bd = B_MN ? sdesc_mn_sw128(sa + Cfg::A_BYTES, 8192) : sdesc_k_sw128(sa + Cfg::A_BYTES);
+            const uint64_t ad = ad0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = bd0 + (uint32_t)(s * (Cfg::STAGE / 16));
             const int nk = kb == t.kbs - 1 ? (t.ktail + 15) / 16 : GT_BK / 16;
-            if (elect_one()) {
+            if (n > 0) {
 #pragma unroll
               for (int k = 0; k < GT_BK / 16; ++k)
-                if (k < nk)
-                  pair_mma<CTAS, false>(d, ad + (A_MN ? 128u : 2u) * k, bd + (B_MN ? 128u : 2u) * k, idesc,
-                                        (kb == kc && k == 0) ? 0u : 1u);
-              pair_commit<CTAS>(&empty[s]);
+                if (k < nk) pair_mma<CTAS, false>(d, ad + AK * k, bd + BK * k, idesc, (kb == kc && k == 0) ? 0u : 1u);
             }
-            __syncwarp();
+            pair_commit<CTAS>(&empty[s]);
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1;
+            }
           }
-          if (ok && elect_one()) pair_commit<CTAS>(&accfull[b]);
-          __syncwarp();
+          if (ok) pair_commit<CTAS>(&accfull[b]);
+          b ^= 1;
+          if (!b) bph ^= 1;
         }
       }
-      if (elect_one()) pair_commit<CTAS>(mma_done);
-      __syncwarp();
+      pair_commit<CTAS>(mma_done);
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------- epilogue
     constexpr int NCH = (BN + 63) / 64;   // 32-column pieces per warpgroup

@@ -297,7 +297,7 @@ sffn_status qlinear_rows(const sffn_qlinear_handle* h, const void* xq, QlinArgs 
   // columns per tile: what gives the least rounds x columns (a tile also costs
   // about 32 columns' time whatever its width)
   long long best = -1;
-  for (int n = 256; n >= 64; n -= 32) {
+  for (int n = 256; n >= 64; n -= 64) {
     const long long cost = ((mt * cdiv(a.n, n) + slots - 1) / slots) * (n + 32);
     if (best < 0 || cost < best) {
       best = cost;
@@ -422,13 +422,11 @@ cudaError_t grouped_attr() {
 template <int MODE, int CTAS, int BN>
 sffn_status grouped_launch(const sffn_grouped_handle* h, const CUtensorMap& mA, const void* cols, long long inner,
                            const GroupedArgs& g, long long tiles, cudaStream_t st) {
-  CUtensorMap mB, mB32;
-  if (!grouped_map(&mB, cols, inner, g.R, 0, MODE == GROUPED_DW ? 64 : GtCfg<CTAS, BN>::B_ROWS)) return SFFN_ERR_CUDA;
-  if (MODE == GROUPED_DW) mB32 = mB;
-  else if (!grouped_map(&mB32, cols, inner, g.R, 0, 32)) return SFFN_ERR_CUDA;
+  CUtensorMap mB;
+  if (!grouped_map(&mB, cols, inner, g.R, 0, MODE == GROUPED_DW ? 64 : GtCfg<CTAS, BN>::BOX)) return SFFN_ERR_CUDA;
   const int grid = (int)std::min<long long>(tiles, h->n_sm / CTAS) * CTAS;
   return launched(launch_pdl(k_grouped<MODE, CTAS, BN>, dim3(grid), dim3(GT_THREADS), (size_t)GtCfg<CTAS, BN>::SMEM, st,
-                             CTAS, mA, mB, mB32, g));
+                             CTAS, mA, mB, g));
 }
 
 // Products over the rows of every group (forward, input gradient).

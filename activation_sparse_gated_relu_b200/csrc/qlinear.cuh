@@ -27,8 +27,8 @@ namespace sffn {
 
 constexpr int QL_SMEM = 227 * 1024;
 constexpr int QL_EPI_WARPS = 8;
-constexpr int QL_PRODUCER = QL_EPI_WARPS, QL_MMA = QL_EPI_WARPS + 1, QL_SCALE = QL_EPI_WARPS + 2;
-constexpr int QL_THREADS = (QL_EPI_WARPS + 3) * 32;
+constexpr int QL_PRODUCER = QL_EPI_WARPS, QL_SCALE = QL_EPI_WARPS + 1, QL_MMA = QL_EPI_WARPS + 2;   // QL_MMA, + 1
+constexpr int QL_THREADS = (QL_EPI_WARPS + 4) * 32;
 
 // Instruction descriptor, kind::f8f6f4: e4m3 x e4m3 -> fp32, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
@@ -54,13 +54,17 @@ __device__ __forceinline__ void put_y(void* y, int f32, size_t at, float v) {
 
 template <int BN>
 struct QcCfg {
-  static constexpr int KS = BN <= 32 ? 4 : BN <= 64 ? 2 : 1;   // 128-wide blocks per stage
+  static constexpr int KS = BN <= 64 ? 2 : 1;            // 128-wide blocks per stage
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = KS * (A_BYTES + B_BYTES);
   static constexpr int SCALES = KS * BN * 4;             // a stage's xs, [KS][BN]
   static constexpr int FIXED = 1024 + 512;
+  // An even number: the MMA threads and (up to 64 columns) the epilogue
+  // warpgroups take every other stage, and each may only ever wait on barriers
+  // whose every phase it waits for: a phase's parity says nothing about the
+  // phases it has not seen.
   static constexpr int RAW = (QL_SMEM - FIXED) / (STAGE + SCALES);
-  static constexpr int STAGES = RAW > 8 ? 8 : RAW;
+  static constexpr int STAGES = (RAW > 8 ? 8 : RAW) & ~1;
   static constexpr int SMEM = FIXED + STAGES * (STAGE + SCALES);
   static constexpr int NBUF = 4;                         // TMEM accumulators, KS · BN columns each
   // Up to 64 columns the two epilogue warpgroups take every other stage, above
@@ -109,7 +113,7 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       mbar_init(&accfull[b], 1);
       mbar_init(&accfree[b], Cfg::ALT ? 4 : QL_EPI_WARPS);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -183,17 +187,20 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
         ph ^= 1;
       }
     }
-  } else if (warp == QL_MMA) {
-    // ----------------------------------------------------------- MMA issuer
+  } else if (warp >= QL_MMA) {
+    // ---------------------------------------------------------- MMA issuers
+    // One thread of each of two warps, every other stage each: an MMA's issue
+    // waits for the one before it, so what a thread does between its MMAs
+    // (looking at barriers, mostly) leaves the tensor core idle unless another
+    // thread's are there.
     const uint32_t idesc = idesc_e4m3_f32(128, bn);
     const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
     if (elect_one()) {
-      bool ok = true;
-      int s = 0, b = 0;
-      uint32_t ph = 0, bph = 1;        // phase of full[s]; of accfree[b] (free in the first round)
-      for (int i = 0; i < ns; ++i) {
-        ok = mbar_wait(&full[s], ph, abort_flag, a.status) && mbar_wait(&accfree[b], bph, abort_flag, a.status);
-        if (!ok) break;
+      for (int i = warp - QL_MMA; i < ns; i += 2) {
+        const int s = i % STAGES, b = i % NBUF;
+        if (!mbar_wait(&full[s], (i / STAGES) & 1, abort_flag, a.status) ||
+            !mbar_wait(&accfree[b], (i / NBUF + 1) & 1, abort_flag, a.status))   // free in the first round
+          break;
         tc_fence_after();
         const uint64_t ad = desc0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = ad + KS * (Cfg::A_BYTES / 16);
         const int nb = min(KS, kb1 - kb0 - i * KS);
@@ -207,14 +214,6 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
           }
         tc_commit(&accfull[b]);
         tc_commit(&empty[s]);
-        if (++b == NBUF) {
-          b = 0;
-          bph ^= 1;
-        }
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1;
-        }
       }
       tc_commit(mma_done);
     }
@@ -331,11 +330,14 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 }
 
 // ---------------------------------------------------------------- many tokens
-// Sixteen epilogue warps: a block's sums have to leave TMEM and be scaled in the
-// time of four MMAs, and every step of that (wait, load, signal) is latency.
+// Every block's sums (128 x 256 per CTA) are read from TMEM, at 64 bytes a
+// cycle per quarter of it: 512 cycles, as long as the block's MMAs take.  So
+// that neither waits for the other, a tile is computed in two halves of its
+// columns with two accumulators each, four in all, and sixteen warps read
+// them, eight to a half.
 constexpr int QR_EPI_WARPS = 16;
-constexpr int QR_PRODUCER = QR_EPI_WARPS, QR_MMA = QR_EPI_WARPS + 1, QR_SCALE = QR_EPI_WARPS + 2;
-constexpr int QR_THREADS = (QR_EPI_WARPS + 3) * 32;
+constexpr int QR_PRODUCER = QR_EPI_WARPS, QR_SCALE = QR_EPI_WARPS + 1, QR_MMA = QR_EPI_WARPS + 2;   // QR_MMA, + 1
+constexpr int QR_THREADS = (QR_EPI_WARPS + 4) * 32;
 constexpr int QR_SLOT = 132;    // floats of one block's scales: 128 tokens, up to 3 weight blocks
 
 template <int CTAS>
@@ -348,24 +350,24 @@ struct QrCfg {
   static constexpr int SMEM = FIXED + STAGES * STAGE;
 };
 
-// Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (a multiple of 32).
+// Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (a multiple of 64).
 template <int CTAS>
 __global__ void __launch_bounds__(QR_THREADS, 1)
 k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW, const QlinArgs a) {
   using Cfg = QrCfg<CTAS>;
-  constexpr int STAGES = Cfg::STAGES, BN = Cfg::BN;
+  constexpr int STAGES = Cfg::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * Cfg::STAGE);
   uint64_t* empty = full + STAGES;
-  uint64_t* accfull = empty + STAGES;   // [2]
-  uint64_t* accfree = accfull + 2;      // [2]
-  uint64_t* sfree = accfree + 2;        // [2] this CTA's epilogue is done with a slot of scales
+  uint64_t* accfull = empty + STAGES;   // [2 accumulators][2 halves]
+  uint64_t* accfree = accfull + 4;      // [2][2]
+  uint64_t* sfree = accfree + 4;        // [2] this CTA's epilogue is done with a slot of scales
   uint64_t* mma_done = sfree + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* slots = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE + 256);   // [2][QR_SLOT]
-  static_assert((2 * STAGES + 7) * 8 + 8 <= 256, "barrier area");
+  static_assert((2 * STAGES + 11) * 8 + 8 <= 256, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
@@ -375,14 +377,14 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], CTAS);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);          // both halves' MMAs have read it
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&accfull[b], 2);        // the MMAs' sums, and their scales
-      mbar_init(&accfree[b], QR_EPI_WARPS * CTAS);
-      mbar_init(&sfree[b], QR_EPI_WARPS);
+    for (int q = 0; q < 4; ++q) {
+      mbar_init(&accfull[q], 2);        // the MMAs' sums, and their scales
+      mbar_init(&accfree[q], QR_EPI_WARPS / 2 * CTAS);
     }
-    mbar_init(mma_done, 1);
+    for (int b = 0; b < 2; ++b) mbar_init(&sfree[b], QR_EPI_WARPS);
+    mbar_init(mma_done, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -468,7 +470,7 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
               for (int i = 0; i < 4; ++i) slot[i * 32 + lane] = v[j][i];
               if (lane < 3) slot[128 + lane] = v[j][4];
               __syncwarp();
-              if (lane == 0) mbar_arrive(&accfull[b]);
+              if (lane < 2) mbar_arrive(&accfull[2 * b + lane]);
               b ^= 1;
               if (!b) bph ^= 1;
             }
@@ -476,86 +478,82 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
         }
       }
     }
-  } else if (warp == QR_MMA) {
-    // ----------------------------------------------------------- MMA issuer
-    // One thread (of the pair's first CTA).  An MMA's issue waits for the one
-    // before it, so the next block's barriers are looked at between this
-    // block's MMAs: a wait after them would leave the tensor core idle.
+  } else if (warp >= QR_MMA) {
+    // ---------------------------------------------------------- MMA issuers
+    // One thread of each of two warps (of the pair's first CTA), a half of the
+    // columns each: see k_qlinear_cols.
+    const int hf = warp - QR_MMA;
     if (rank == 0 && elect_one()) {
-      const uint32_t idesc = idesc_e4m3_f32(128 * CTAS, a.each);
+      const uint32_t idesc = idesc_e4m3_f32(128 * CTAS, a.each / 2);
       const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
-      bool ok = true, there = false, free = true;
+      const uint32_t b_half = Cfg::A_BYTES / 16 + (uint32_t)(hf * (half / 2)) * (128 / 16);   // its rows of this CTA's B
+      bool ok = true;
       int s = 0, b = 0;
       uint32_t ph = 0, bph = 1;        // phase of full[s]; of accfree[b] (free in the first round)
       for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
         for (int kb = 0; kb < KB; ++kb) {
-          if (!there) ok = mbar_wait(&full[s], ph, abort_flag, a.status);
-          if (ok && !free) ok = mbar_wait(&accfree[b], bph, abort_flag, a.status);
+          ok = mbar_wait(&full[s], ph, abort_flag, a.status) && mbar_wait(&accfree[2 * b + hf], bph, abort_flag, a.status);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t ad = desc0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = ad + Cfg::A_BYTES / 16;
-          const uint32_t d = tmem + (uint32_t)(b * BN);
-          uint64_t *const done = &accfull[b], *const used = &empty[s];
-          pair_mma<CTAS, true>(d, ad, bd, idesc, 0u);
-          pair_mma<CTAS, true>(d, ad + 2, bd + 2, idesc, 1u);
-          pair_mma<CTAS, true>(d, ad + 4, bd + 4, idesc, 1u);
+          const uint64_t ad = desc0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = ad + b_half;
+          const uint32_t d = tmem + (uint32_t)((2 * b + hf) * 128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pair_mma<CTAS, true>(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+          pair_commit<CTAS>(&accfull[2 * b + hf]);
+          pair_commit<CTAS>(&empty[s]);
           b ^= 1;
           if (!b) bph ^= 1;
           if (++s == STAGES) {
             s = 0;
             ph ^= 1;
           }
-          there = mbar_test(&full[s], ph);
-          free = mbar_test(&accfree[b], bph);
-          pair_mma<CTAS, true>(d, ad + 6, bd + 6, idesc, 1u);
-          pair_commit<CTAS>(done);
-          pair_commit<CTAS>(used);
         }
       }
       pair_commit<CTAS>(mma_done);
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------- epilogue
-    // A thread has one token and every fourth 16 columns of the tile: at most
-    // 64.  The tile touches up to three weight blocks.
-    const int wg = warp >> 2;
-    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t free0 = CTAS == 2 ? cluster_addr(smem_u32(&accfree[0]), 0) : smem_u32(&accfree[0]);
+    // A thread has one token and a quarter of the tile's columns, at most 64,
+    // which touch at most two weight blocks (the second from column `edge` on).
+    const int wg = warp >> 2, hf = wg >> 1, sub = wg & 1, quarter = a.each / 4;
+    const int first = CTAS == 2 ? sub * 2 * quarter + hf * quarter : wg * quarter;   // of the tile's columns
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(hf * 128 + sub * quarter);
+    const uint32_t free0 = CTAS == 2 ? cluster_addr(smem_u32(&accfree[hf]), 0) : smem_u32(&accfree[hf]);
     int b = 0;
     uint32_t bph = 0;
     bool ok = true;
     for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
       const int t = (w % mt * CTAS + (int)rank) * 128 + (warp & 3) * 32 + lane;
-      const int n0 = w / mt * a.each;
-      const int edge = Q_GROUP - (n0 & (Q_GROUP - 1));   // first column of the second block
+      const int t0 = w / mt * a.each, n0 = t0 + first;
+      const int blk = n0 / Q_GROUP - t0 / Q_GROUP, edge = Q_GROUP - (n0 & (Q_GROUP - 1));
       float acc[4][16];
 #pragma unroll
       for (int p = 0; p < 4; ++p)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[p][i] = 0.0f;
       for (int kb = 0; kb < KB; ++kb) {
-        ok = mbar_wait_warp(&accfull[b], bph, abort_flag, a.status);
+        ok = mbar_wait_warp(&accfull[2 * b + hf], bph, abort_flag, a.status);
         if (!ok) break;
         tc_fence_after();
         const float* slot = slots + b * QR_SLOT;
         const float x = slot[(warp & 3) * 32 + lane];
-        const float s0 = x * slot[128], s1 = x * slot[129], s2 = x * slot[130];
+        const float s0 = x * slot[128 + blk], s1 = x * slot[128 + min(blk + 1, 2)];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           // without a test for narrower tiles: what their unused columns hold is
           // never stored, and a test would cost a select per sum
-          const int c = 64 * p + 16 * wg;
           float v[16];
-          tmem_get16(tlane + (uint32_t)(b * BN + c), v);
-          const float sc = c < edge ? s0 : c < edge + Q_GROUP ? s1 : s2;
+          tmem_get16(tlane + (uint32_t)(b * 256 + 16 * p), v);
+          const float sc = 16 * p < edge ? s0 : s1;
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[p][i] = fmaf(v[i], sc, acc[p][i]);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (CTAS == 2) mbar_arrive_cluster(free0 + 8 * b);
-          else mbar_arrive(&accfree[b]);
+          if (CTAS == 2) mbar_arrive_cluster(free0 + 16 * b);
+          else mbar_arrive(&accfree[2 * b + hf]);
           mbar_arrive(&sfree[b]);
         }
         b ^= 1;
@@ -567,8 +565,8 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
         for (int p = 0; p < 4; ++p) {
 #pragma unroll
           for (int i = 0; i < 16; i += 8) {
-            const int c = 64 * p + 16 * wg + i;
-            if (c < a.each && n0 + c < a.n) {   // both multiples of 8
+            const int c = 16 * p + i;
+            if (c < quarter && n0 + c < a.n) {   // both multiples of 8
               float v[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) v[j] = acc[p][i + j];

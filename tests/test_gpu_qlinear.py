@@ -41,7 +41,8 @@ def check(op, xq, xs, out="bf16"):
 
 SHAPES = [(1, 16, 8), (1, 128, 128), (2, 144, 136), (7, 256, 1000), (8, 4096, 512), (13, 1040, 264), (16, 512, 256),
           (17, 400, 128), (33, 2048, 384), (64, 272, 520), (65, 256, 256), (100, 1024, 1032), (128, 4096, 256),
-          (129, 144, 8), (257, 640, 392), (333, 2048, 512), (520, 512, 1544), (1000, 1168, 640)]
+          (129, 144, 8), (257, 640, 392), (333, 2048, 512), (520, 512, 1544), (1000, 1168, 640),
+          (3, 4096, 9728), (20, 4096, 9728), (40, 4096, 9728), (70, 4224, 9728), (2, 14336, 264)]
 
 
 @pytest.mark.parametrize("T,k,n", SHAPES)
@@ -53,8 +54,8 @@ def test_random_codes(T, k, n, out):
 
 @pytest.mark.parametrize("T,k,n", SHAPES)
 def test_exact_sums(T, k, n):
-    # codes in -3..3 and scales 2^-2..2^2: every partial sum is a multiple of 2^-4 below 2^20 for k <= 4096,
-    # so fp32 holds all of them exactly and any order of additions gives the same sum
+    # codes in -3..3 and scales 2^-2..2^2: every partial sum is a multiple of 2^-4 below 9 · 16 · 14336 < 2^21,
+    # 25 bits at most with sums that stay far below that bound: fp32 holds all of them exactly and any order of additions gives the same sum
     xq, Wq = ints(3, T, k, lim=3, dtype=F32).to(F8), ints(4, n, k, lim=3, dtype=F32).to(F8)
     xs = torch.exp2(torch.randint(-2, 3, (T, groups(k)), generator=gen(5)).float()).cuda()
     Ws = torch.exp2(torch.randint(-2, 3, (groups(n), groups(k)), generator=gen(6)).float()).cuda()
