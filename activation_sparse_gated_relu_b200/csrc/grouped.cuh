@@ -343,15 +343,15 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t free0 = CTAS == 2 ? cluster_addr(smem_u32(&accfree[0]), 0) : smem_u32(&accfree[0]);
     int ci = 0;
-    bool ok = true;
-    for (int w = walk0; w < n_tiles && ok; w += n_walk) {
+    // Left at once when a wait fails: leaving the inner loop from its middle
+    // would keep both sides' sums alive, a select for each of them.
+    auto run = [&]() {
+    for (int w = walk0; w < n_tiles; w += n_walk) {
       t.set(w);
       float acc[NCH][32];
       for (int kc = 0; kc < t.kbs; kc += args.kchunk, ++ci) {
         const int b = ci & 1;
-        // the loads from TMEM are warp-wide: all lanes go on, or none
-        ok = mbar_wait_warp(&accfull[b], (uint32_t)((ci >> 1) & 1), abort_flag, args.status);
-        if (!ok) break;
+        if (!mbar_wait_warp(&accfull[b], (uint32_t)((ci >> 1) & 1), abort_flag, args.status)) return;
         tc_fence_after();
         // all of the tile's columns, computed or not: what the others hold is
         // never stored, and a test would cost a select per value
@@ -375,7 +375,6 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
           else mbar_arrive(&accfree[b]);
         }
       }
-      if (!ok) break;
       if (MODE == GROUPED_DW && t.kbs == 0) {
 #pragma unroll
         for (int j = 0; j < NCH; ++j)
@@ -415,6 +414,8 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         }
       }
     }
+    };
+    run();
   }
   __syncwarp();
   tc_fence_before();

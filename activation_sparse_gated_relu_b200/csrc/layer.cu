@@ -297,7 +297,7 @@ sffn_status qlinear_rows(const sffn_qlinear_handle* h, const void* xq, QlinArgs 
   // columns per tile: what gives the least rounds x columns (a tile also costs
   // about 32 columns' time whatever its width)
   long long best = -1;
-  for (int n = 256; n >= 64; n -= 64) {
+  for (int n = 256; n >= 64; n -= 32) {
     const long long cost = ((mt * cdiv(a.n, n) + slots - 1) / slots) * (n + 32);
     if (best < 0 || cost < best) {
       best = cost;

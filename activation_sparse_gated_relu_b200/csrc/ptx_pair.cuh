@@ -63,6 +63,17 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
 }
 
+// Four bytes from global to shared memory, asynchronously; zero where `in` is false.
+__device__ __forceinline__ void copy4_async(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0)
+               : "memory");
+}
+// One arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Tiled loads into this CTA's shared memory; `bar` is a cluster address, with
 // a pair possibly in the other CTA.  c0 · element size is a multiple of 16.
 template <int CTAS>
@@ -173,6 +184,24 @@ __device__ __forceinline__ void tmem_get32(uint32_t taddr, float (&v)[32]) {
       : "memory");
 }
 
+// The same load in two steps, for work between them: the values may be used
+// after tmem_have16, which takes them as operands so that no use moves before it.
+__device__ __forceinline__ void tmem_ask16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_have16(float (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
 // Shared-memory descriptor of an MN-major operand staged by TMA with
 // SWIZZLE_128B: rows of 64 values along M or N (128 bytes), one row per k;
 // 8-row groups 1024 bytes apart, the next 64 values of M or N `chunk` bytes

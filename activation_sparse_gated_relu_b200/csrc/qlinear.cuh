@@ -57,7 +57,8 @@ struct QcCfg {
   static constexpr int KS = BN <= 64 ? 2 : 1;            // 128-wide blocks per stage
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = KS * (A_BYTES + B_BYTES);
-  static constexpr int SCALES = KS * BN * 4;             // a stage's xs, [KS][BN]
+  static constexpr int SLOT = BN + 4;                    // scales of a block: tokens, two weight blocks
+  static constexpr int SCALES = KS * SLOT * 4;
   static constexpr int FIXED = 1024 + 512;
   // An even number: the MMA threads and (up to 64 columns) the epilogue
   // warpgroups take every other stage, and each may only ever wait on barriers
@@ -82,7 +83,7 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   static_assert(NCOLS >= 32 && NCOLS <= 512 && (NCOLS & (NCOLS - 1)) == 0, "TMEM columns");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* s_xs = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE);   // [STAGES][KS][BN]
+  float* slots = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE);  // [STAGES][KS][SLOT]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * (Cfg::STAGE + Cfg::SCALES));
   uint64_t* empty = full + STAGES;
   uint64_t* sfull = empty + STAGES;     // a stage's scales are there / have been used
@@ -106,7 +107,7 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&sfull[s], 1);
+      mbar_init(&sfull[s], 32);
       mbar_init(&sempty[s], Cfg::ALT ? 4 : QL_EPI_WARPS);
     }
     for (int b = 0; b < NBUF; ++b) {
@@ -161,32 +162,29 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
     }
   } else if (warp == QL_SCALE) {
-    // --------------------------------------------- the tokens' scales, by stage
-    constexpr int NC = (BN + 31) / 32;
+    // ----------------------------------------------------- scales, by stage
     int s = 0;
     uint32_t ph = 1;
+    const int nblk = (a.n + Q_GROUP - 1) / Q_GROUP;
+    const float* ws = a.Ws + (size_t)min(m0 / Q_GROUP + (lane & 1), nblk - 1) * a.kb;
     for (int i = 0; i < ns; ++i) {
-      float v[KS][NC];
+      if (!mbar_wait_warp(&sempty[s], ph, abort_flag, a.status)) break;   // the first round passes
 #pragma unroll
-      for (int j = 0; j < KS; ++j)
+      for (int j = 0; j < KS; ++j) {
+        const int kb = min(kb0 + i * KS + j, kb1 - 1);
+        float* slot = slots + (s * KS + j) * Cfg::SLOT;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int kb = kb0 + i * KS + j, col = c * 32 + lane;
-          v[j][c] = kb < kb1 && col < cols ? a.xs[(size_t)(n0 + col) * a.kb + kb] : 0.0f;
-        }
-      if (!mbar_wait_warp(&sempty[s], ph, abort_flag, a.status)) break;
-#pragma unroll
-      for (int j = 0; j < KS; ++j)
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-          if (c * 32 + lane < BN) s_xs[(s * KS + j) * BN + c * 32 + lane] = v[j][c];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sfull[s]);
+        for (int col = lane; col < BN; col += 32)
+          copy4_async(slot + col, a.xs + (size_t)(n0 + min(col, cols - 1)) * a.kb + kb, col < cols);
+        if (lane < 2) copy4_async(slot + BN + lane, ws + kb, true);
+      }
+      copies_arrive(&sfull[s]);
       if (++s == STAGES) {
         s = 0;
         ph ^= 1;
       }
     }
+    copies_wait_all();
   } else if (warp >= QL_MMA) {
     // ---------------------------------------------------------- MMA issuers
     // One thread of each of two warps, every other stage each: an MMA's issue
@@ -234,23 +232,23 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     const int c0 = Cfg::ALT ? 0 : wg * COLS;            // first column of this thread
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const bool in = row < a.h && m < a.n;
-    const float* ws = a.Ws + (size_t)(in ? m / Q_GROUP : 0) * a.kb;
+    const int blk = in ? m / Q_GROUP - m0 / Q_GROUP : 0;   // h <= 128: one of two weight blocks
     float acc[COLS];
 #pragma unroll
     for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
     for (int i = Cfg::ALT ? wg : 0; i < ns; i += Cfg::ALT ? 2 : 1) {
       const int s = i % STAGES, b = i % NBUF, kb = kb0 + i * KS;
-      float w[KS];
-#pragma unroll
-      for (int j = 0; j < KS; ++j) w[j] = kb + j < kb1 ? ws[kb + j] : 0.0f;
-      if (!mbar_wait_warp(&sfull[s], (i / STAGES) & 1, abort_flag, a.status) ||
-          !mbar_wait_warp(&accfull[b], (i / NBUF) & 1, abort_flag, a.status))
-        break;
+      // A failed wait is not acted on (nothing is stored then): leaving the
+      // loop from its middle would cost a select per sum.
+      mbar_wait_warp(&sfull[s], (i / STAGES) & 1, abort_flag, a.status);
+      mbar_wait_warp(&accfull[b], (i / NBUF) & 1, abort_flag, a.status);
       tc_fence_after();
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
         if (kb + j < kb1) {
-          const float4* xs = reinterpret_cast<const float4*>(s_xs + (s * KS + j) * BN + c0);
+          const float* slot = slots + (s * KS + j) * Cfg::SLOT;
+          const float4* xs = reinterpret_cast<const float4*>(slot + c0);
+          const float w = slot[BN + blk];
 #pragma unroll
           for (int c = 0; c < COLS; c += 16) {
             float v[16];
@@ -258,10 +256,10 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 #pragma unroll
             for (int u = 0; u < 16; u += 4) {
               const float4 x = xs[(c + u) / 4];
-              acc[c + u] = fmaf(v[u], x.x * w[j], acc[c + u]);
-              acc[c + u + 1] = fmaf(v[u + 1], x.y * w[j], acc[c + u + 1]);
-              acc[c + u + 2] = fmaf(v[u + 2], x.z * w[j], acc[c + u + 2]);
-              acc[c + u + 3] = fmaf(v[u + 3], x.w * w[j], acc[c + u + 3]);
+              acc[c + u] = fmaf(v[u], x.x * w, acc[c + u]);
+              acc[c + u + 1] = fmaf(v[u + 1], x.y * w, acc[c + u + 1]);
+              acc[c + u + 2] = fmaf(v[u + 2], x.z * w, acc[c + u + 2]);
+              acc[c + u + 3] = fmaf(v[u + 3], x.w * w, acc[c + u + 3]);
             }
           }
         }
@@ -330,61 +328,65 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 }
 
 // ---------------------------------------------------------------- many tokens
-// Every block's sums (128 x 256 per CTA) are read from TMEM, at 64 bytes a
-// cycle per quarter of it: 512 cycles, as long as the block's MMAs take.  So
-// that neither waits for the other, a tile is computed in two halves of its
-// columns with two accumulators each, four in all, and sixteen warps read
-// them, eight to a half.
-constexpr int QR_EPI_WARPS = 16;
-constexpr int QR_PRODUCER = QR_EPI_WARPS, QR_SCALE = QR_EPI_WARPS + 1, QR_MMA = QR_EPI_WARPS + 2;   // QR_MMA, + 1
+// Every block's sums (128 x 256 per CTA) pass from TMEM through registers, in
+// the time of the next block's four MMAs (512 cycles): 128 columns per thread,
+// 128 of its registers their sums, two pieces of 16 columns in flight (one
+// read while the other is multiplied).  384 threads leave 168 registers each.
+constexpr int QR_EPI_WARPS = 8;
+constexpr int QR_PRODUCER = QR_EPI_WARPS, QR_SCALE = QR_EPI_WARPS + 1, QR_MMA = QR_EPI_WARPS + 2;   // + 3 idles
 constexpr int QR_THREADS = (QR_EPI_WARPS + 4) * 32;
-constexpr int QR_SLOT = 132;    // floats of one block's scales: 128 tokens, up to 3 weight blocks
-
+// Scales of a block: 128 tokens, up to 3 weight blocks.  Every token's come
+// from another line, with the latency of L2: 16 blocks of them are in flight.
+constexpr int QR_SLOTS = 16, QR_SLOT = 132;
 template <int CTAS>
 struct QrCfg {
   static constexpr int BN = 256;                        // weight rows per tile, at most
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / CTAS * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int FIXED = 1024 + 256 + 2 * QR_SLOT * 4;
+  static constexpr int FIXED = 1024 + 512 + QR_SLOTS * QR_SLOT * 4;
   static constexpr int STAGES = (QL_SMEM - FIXED) / STAGE;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
 };
 
-// Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (a multiple of 64).
+// Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (a multiple of 32).
 template <int CTAS>
 __global__ void __launch_bounds__(QR_THREADS, 1)
 k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW, const QlinArgs a) {
   using Cfg = QrCfg<CTAS>;
-  constexpr int STAGES = Cfg::STAGES;
+  constexpr int STAGES = Cfg::STAGES, BN = Cfg::BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * Cfg::STAGE);
   uint64_t* empty = full + STAGES;
-  uint64_t* accfull = empty + STAGES;   // [2 accumulators][2 halves]
-  uint64_t* accfree = accfull + 4;      // [2][2]
-  uint64_t* sfree = accfree + 4;        // [2] this CTA's epilogue is done with a slot of scales
-  uint64_t* mma_done = sfree + 2;
+  uint64_t* accfull = empty + STAGES;   // [2]
+  uint64_t* accfree = accfull + 2;      // [2]; the second CTA's epilogue signals its own, see the relay
+  uint64_t* sfull = accfree + 2;        // [QR_SLOTS] scales
+  uint64_t* sfree = sfull + QR_SLOTS;
+  uint64_t* mma_done = sfree + QR_SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* slots = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE + 256);   // [2][QR_SLOT]
-  static_assert((2 * STAGES + 11) * 8 + 8 <= 256, "barrier area");
+  float* slots = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE + 512);   // [QR_SLOTS][QR_SLOT]
+  static_assert((2 * STAGES + 5 + 2 * QR_SLOTS) * 8 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
   const int mt = (a.T + 128 * CTAS - 1) / (128 * CTAS), n_tiles = mt * ((a.n + a.each - 1) / a.each);
-  const int KB = a.kb, half = a.each / CTAS;
+  const int KB = a.kb, half = a.each / CTAS, walk0 = blockIdx.x / CTAS, n_walk = gridDim.x / CTAS;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], CTAS);
-      mbar_init(&empty[s], 2);          // both halves' MMAs have read it
+      mbar_init(&empty[s], 1);
     }
-    for (int q = 0; q < 4; ++q) {
-      mbar_init(&accfull[q], 2);        // the MMAs' sums, and their scales
-      mbar_init(&accfree[q], QR_EPI_WARPS / 2 * CTAS);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accfree[b], QR_EPI_WARPS + (CTAS == 2 && rank == 0 ? 1 : 0));
     }
-    for (int b = 0; b < 2; ++b) mbar_init(&sfree[b], QR_EPI_WARPS);
-    mbar_init(mma_done, 2);
+    for (int j = 0; j < QR_SLOTS; ++j) {
+      mbar_init(&sfull[j], 32);
+      mbar_init(&sfree[j], QR_EPI_WARPS);
+    }
+    mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -393,6 +395,7 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     tma_prefetch_desc(&mX);
     tma_prefetch_desc(&mW);
   }
+  __syncwarp();
   tc_fence_before();
   if (CTAS == 2) cluster_sync();   // the barriers of both CTAs are ready
   __syncthreads();
@@ -400,184 +403,199 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
   const uint32_t tmem = *tmem_slot;
   griddep_wait();   // operands and outputs belong to the stream order
 
-  if (warp == QR_PRODUCER) {
-    // --------------------------------------------------------- TMA producer
-    bool ok = true;
-    int s = 0;
-    uint32_t ph = 1;
-    for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
-      const int m0 = (w % mt * CTAS + (int)rank) * 128, n0 = w / mt * a.each + (int)rank * half;
-      for (int kb = 0; kb < KB; ++kb) {
-        ok = mbar_wait_warp(&empty[s], ph, abort_flag, a.status);   // the first round passes
-        if (!ok) break;
-        if (elect_one()) {
-          uint8_t* st = smem + (size_t)s * Cfg::STAGE;
-          const uint32_t bytes = (uint32_t)(128 + half) * 128;
-          const uint32_t bar = CTAS == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-          if (CTAS == 2) mbar_expect_cluster(bar, bytes);
-          else mbar_expect_tx(&full[s], bytes);
-          tma_2d<CTAS>(st, &mX, bar, kb * 128, m0);
-          tma_2d<CTAS>(st + Cfg::A_BYTES, &mW, bar, kb * 128, n0);
-        }
-        __syncwarp();
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-    }
-    if (!ok) {   // a CTA must not exit before its copies have landed: wait far longer than they take
-      const uint64_t t0 = globaltimer();
-      while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
-    }
-  } else if (warp == QR_SCALE) {
-    // -------------------------------------------- scales, a block ahead of use
-    // The next four blocks' values are in flight while this block's are written.
-    int b = 0;
-    uint32_t bph = 1;
-    bool ok = true;
-    for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
-      const int m0 = (w % mt * CTAS + (int)rank) * 128, nb0 = w / mt * a.each / Q_GROUP;
-      const int nblk = (a.n + Q_GROUP - 1) / Q_GROUP;
-      const float* x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = a.xs + (size_t)min(m0 + i * 32 + lane, a.T - 1) * KB;
-      const float* ws = a.Ws + (size_t)min(nb0 + min(lane, 2), nblk - 1) * KB;
-      float v[4][5], n[4][5];
-      auto fetch = [&](int kb, float (&f)[4][5]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = min(kb + j, KB - 1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[j][i] = x[i][k];
-          f[j][4] = ws[k];
-        }
-      };
-      fetch(0, n);
-      for (int kb = 0; kb < KB && ok; kb += 4) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 5; ++i) v[j][i] = n[j][i];
-        if (kb + 4 < KB) fetch(kb + 4, n);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (kb + j < KB && ok) {
-            ok = mbar_wait_warp(&sfree[b], bph, abort_flag, a.status);   // the first round passes
-            if (ok) {
-              float* slot = slots + b * QR_SLOT;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) slot[i * 32 + lane] = v[j][i];
-              if (lane < 3) slot[128 + lane] = v[j][4];
-              __syncwarp();
-              if (lane < 2) mbar_arrive(&accfull[2 * b + lane]);
-              b ^= 1;
-              if (!b) bph ^= 1;
-            }
-          }
-        }
-      }
-    }
-  } else if (warp >= QR_MMA) {
-    // ---------------------------------------------------------- MMA issuers
-    // One thread of each of two warps (of the pair's first CTA), a half of the
-    // columns each: see k_qlinear_cols.
-    const int hf = warp - QR_MMA;
-    if (rank == 0 && elect_one()) {
-      const uint32_t idesc = idesc_e4m3_f32(128 * CTAS, a.each / 2);
-      const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
-      const uint32_t b_half = Cfg::A_BYTES / 16 + (uint32_t)(hf * (half / 2)) * (128 / 16);   // its rows of this CTA's B
+  if (warp >= QR_EPI_WARPS) {
+    if (warp == QR_PRODUCER) {
+      // ------------------------------------------------------- TMA producer
       bool ok = true;
-      int s = 0, b = 0;
-      uint32_t ph = 0, bph = 1;        // phase of full[s]; of accfree[b] (free in the first round)
-      for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
+      int s = 0;
+      uint32_t ph = 1;
+      for (int w = walk0; w < n_tiles && ok; w += n_walk) {
+        const int m0 = (w % mt * CTAS + (int)rank) * 128, n0 = w / mt * a.each + (int)rank * half;
         for (int kb = 0; kb < KB; ++kb) {
-          ok = mbar_wait(&full[s], ph, abort_flag, a.status) && mbar_wait(&accfree[2 * b + hf], bph, abort_flag, a.status);
+          ok = mbar_wait_warp(&empty[s], ph, abort_flag, a.status);   // the first round passes
           if (!ok) break;
-          tc_fence_after();
-          const uint64_t ad = desc0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = ad + b_half;
-          const uint32_t d = tmem + (uint32_t)((2 * b + hf) * 128);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) pair_mma<CTAS, true>(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-          pair_commit<CTAS>(&accfull[2 * b + hf]);
-          pair_commit<CTAS>(&empty[s]);
-          b ^= 1;
-          if (!b) bph ^= 1;
+          if (elect_one()) {
+            uint8_t* st = smem + (size_t)s * Cfg::STAGE;
+            const uint32_t bytes = (uint32_t)(128 + half) * 128;
+            const uint32_t bar = CTAS == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+            if (CTAS == 2) mbar_expect_cluster(bar, bytes);
+            else mbar_expect_tx(&full[s], bytes);
+            tma_2d<CTAS>(st, &mX, bar, kb * 128, m0);
+            tma_2d<CTAS>(st + Cfg::A_BYTES, &mW, bar, kb * 128, n0);
+          }
+          __syncwarp();
           if (++s == STAGES) {
             s = 0;
             ph ^= 1;
           }
         }
       }
-      pair_commit<CTAS>(mma_done);
+      if (!ok) {   // a CTA must not exit before its copies have landed: wait far longer than they take
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
+      }
+    } else if (warp == QR_SCALE) {
+      // ------------------------------------------------------------- scales
+      const int nblk = (a.n + Q_GROUP - 1) / Q_GROUP;
+      int j = 0;
+      uint32_t jph = 1;
+      bool ok = true;
+      for (int w = walk0; w < n_tiles && ok; w += n_walk) {
+        const int m0 = (w % mt * CTAS + (int)rank) * 128, nb0 = w / mt * a.each / Q_GROUP;
+        const float* x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = a.xs + (size_t)min(m0 + i * 32 + lane, a.T - 1) * KB;
+        const float* ws = a.Ws + (size_t)min(nb0 + min(lane, 2), nblk - 1) * KB;
+        for (int kb = 0; kb < KB; ++kb) {
+          ok = mbar_wait_warp(&sfree[j], jph, abort_flag, a.status);   // the first round passes
+          if (!ok) break;
+          float* slot = slots + j * QR_SLOT;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) copy4_async(slot + i * 32 + lane, x[i] + kb, true);
+          if (lane < 3) copy4_async(slot + 128 + lane, ws + kb, true);
+          copies_arrive(&sfull[j]);
+          if (++j == QR_SLOTS) {
+            j = 0;
+            jph ^= 1;
+          }
+        }
+      }
+      copies_wait_all();
+    } else if (warp == QR_MMA && rank == 0) {
+      // --------------------------------------------------------- MMA issuer
+      // One thread (of the pair's first CTA).
+      if (elect_one()) {
+        const uint32_t idesc = idesc_e4m3_f32(128 * CTAS, a.each);
+        const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
+        bool ok = true;
+        int s = 0, b = 0;
+        uint32_t ph = 0, bph = 1;        // phase of full[s]; of accfree[b] (free in the first round)
+        for (int w = walk0; w < n_tiles && ok; w += n_walk) {
+          for (int kb = 0; kb < KB; ++kb) {
+            ok = mbar_wait(&full[s], ph, abort_flag, a.status) && mbar_wait(&accfree[b], bph, abort_flag, a.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = desc0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = ad + Cfg::A_BYTES / 16;
+            const uint32_t d = tmem + (uint32_t)(b * BN);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pair_mma<CTAS, true>(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+            pair_commit<CTAS>(&accfull[b]);
+            pair_commit<CTAS>(&empty[s]);
+            b ^= 1;
+            if (!b) bph ^= 1;
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+        }
+        pair_commit<CTAS>(mma_done);
+      }
+    } else if (CTAS == 2 && warp == QR_MMA) {
+      // -------------------------------------------------------------- relay
+      // A signal to the other CTA takes a warp some 300 cycles: the second
+      // CTA's epilogue signals here, and this warp passes one signal on.
+      const uint32_t free0 = cluster_addr(smem_u32(&accfree[0]), 0);
+      int b = 0;
+      uint32_t bph = 0;
+      bool ok = true;
+      for (int w = walk0; w < n_tiles && ok; w += n_walk)
+        for (int kb = 0; kb < KB; ++kb) {
+          ok = mbar_wait_warp(&accfree[b], bph, abort_flag, a.status);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_cluster(free0 + 8 * b);
+          b ^= 1;
+          if (!b) bph ^= 1;
+        }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------- epilogue
-    // A thread has one token and a quarter of the tile's columns, at most 64,
-    // which touch at most two weight blocks (the second from column `edge` on).
-    const int wg = warp >> 2, hf = wg >> 1, sub = wg & 1, quarter = a.each / 4;
-    const int first = CTAS == 2 ? sub * 2 * quarter + hf * quarter : wg * quarter;   // of the tile's columns
-    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(hf * 128 + sub * quarter);
-    const uint32_t free0 = CTAS == 2 ? cluster_addr(smem_u32(&accfree[hf]), 0) : smem_u32(&accfree[hf]);
-    int b = 0;
-    uint32_t bph = 0;
-    bool ok = true;
-    for (int w = blockIdx.x / CTAS; w < n_tiles && ok; w += gridDim.x / CTAS) {
-      const int t = (w % mt * CTAS + (int)rank) * 128 + (warp & 3) * 32 + lane;
-      const int t0 = w / mt * a.each, n0 = t0 + first;
-      const int blk = n0 / Q_GROUP - t0 / Q_GROUP, edge = Q_GROUP - (n0 & (Q_GROUP - 1));
-      float acc[4][16];
+    // A thread has one token and half of the tile's columns, at most 128, which
+    // touch at most two weight blocks (the second from column `edge` on).
+    // Tiles narrower than 256 are read as if they were not: what the unused
+    // columns hold is never stored, and a test would cost a select per sum.
+    const int wg = warp >> 2, hc = a.each / 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(wg * hc);
+    int b = 0, j = 0;
+    uint32_t bph = 0, jph = 0;
+    float s0 = 0.0f, s1 = 0.0f;
+    // the next block's scales, for the tile that it belongs to
+    auto scales = [&](int w) -> bool {
+      if (!mbar_wait_warp(&sfull[j], jph, abort_flag, a.status)) return false;
+      const int t0 = w / mt * a.each, blk = (t0 + wg * hc) / Q_GROUP - t0 / Q_GROUP;
+      const float* slot = slots + j * QR_SLOT;
+      const float x = slot[row];
+      s0 = x * slot[128 + blk];
+      s1 = x * slot[128 + min(blk + 1, 2)];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfree[j]);
+      if (++j == QR_SLOTS) {
+        j = 0;
+        jph ^= 1;
+      }
+      return true;
+    };
+    // Left at once when a wait fails: going on to the end of a loop from the
+    // middle would keep both sides' sums alive, a select for each of them.
+    auto run = [&]() {
+    if (walk0 < n_tiles && !scales(walk0)) return;
+    for (int w = walk0; w < n_tiles; w += n_walk) {
+      const int t = (w % mt * CTAS + (int)rank) * 128 + row, n0 = w / mt * a.each + wg * hc;
+      const int edge = Q_GROUP - (n0 & (Q_GROUP - 1));
+      float acc[128];
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[p][i] = 0.0f;
+      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
       for (int kb = 0; kb < KB; ++kb) {
-        ok = mbar_wait_warp(&accfull[2 * b + hf], bph, abort_flag, a.status);
-        if (!ok) break;
+        if (!mbar_wait_warp(&accfull[b], bph, abort_flag, a.status)) return;
         tc_fence_after();
-        const float* slot = slots + b * QR_SLOT;
-        const float x = slot[(warp & 3) * 32 + lane];
-        const float s0 = x * slot[128 + blk], s1 = x * slot[128 + min(blk + 1, 2)];
+        const uint32_t src = tlane + (uint32_t)(b * BN);
+        const float u0 = s0, u1 = s1;
+        float va[16], vb[16];
+        auto add = [&](int c, const float (&v)[16]) {   // columns c .. c + 15; the edge is a multiple of 16
+          const float u = c < edge ? u0 : u1;
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          // without a test for narrower tiles: what their unused columns hold is
-          // never stored, and a test would cost a select per sum
-          float v[16];
-          tmem_get16(tlane + (uint32_t)(b * 256 + 16 * p), v);
-          const float sc = 16 * p < edge ? s0 : s1;
+          for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(v[i], u, acc[c + i]);
+        };
+        tmem_ask16(src, va);
+        tmem_have16(va);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[p][i] = fmaf(v[i], sc, acc[p][i]);
+        for (int c = 0; c < 128; c += 32) {
+          tmem_ask16(src + c + 16, vb);
+          add(c, va);
+          tmem_have16(vb);
+          if (c < 96) {
+            tmem_ask16(src + c + 32, va);
+            add(c + 16, vb);
+            tmem_have16(va);
+          }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (CTAS == 2) mbar_arrive_cluster(free0 + 16 * b);
-          else mbar_arrive(&accfree[2 * b + hf]);
-          mbar_arrive(&sfree[b]);
-        }
+        if (lane == 0) mbar_arrive(&accfree[b]);
+        add(112, vb);
+        const int w_next = kb + 1 < KB ? w : w + n_walk;
+        if (w_next < n_tiles && !scales(w_next)) return;
         b ^= 1;
         if (!b) bph ^= 1;
       }
-      if (!ok) break;
+      const int cols = min(hc, a.n - n0);   // a multiple of 8
       if (t < a.T) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int c = 0; c < 128; c += 8) {
+          if (c < cols) {
+            float v[8];
 #pragma unroll
-          for (int i = 0; i < 16; i += 8) {
-            const int c = 16 * p + i;
-            if (c < quarter && n0 + c < a.n) {   // both multiples of 8
-              float v[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] = acc[p][i + j];
-              const size_t at = ((size_t)t * a.n + n0 + c) / 8;
-              if (a.y_f32) store8_f32(a.y, at, v);
-              else store8_bf16(a.y, at, v);
-            }
+            for (int i = 0; i < 8; ++i) v[i] = acc[c + i];
+            const size_t at = ((size_t)t * a.n + n0 + c) / 8;
+            if (a.y_f32) store8_f32(a.y, at, v);
+            else store8_bf16(a.y, at, v);
           }
         }
       }
     }
+    };
+    run();
   }
   __syncwarp();
   tc_fence_before();
