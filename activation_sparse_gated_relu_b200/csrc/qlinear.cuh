@@ -520,10 +520,11 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     int b = 0, j = 0;
     uint32_t bph = 0, jph = 0;
     float s0 = 0.0f, s1 = 0.0f;
-    // the next block's scales, for the tile that it belongs to
-    auto scales = [&](int w) -> bool {
+    // this half's first weight block, counted from the tile's first
+    auto block_of = [&](int w) { return (w / mt * a.each + wg * hc) / Q_GROUP - w / mt * a.each / Q_GROUP; };
+    // the next block's scales, for a tile whose block_of is blk
+    auto scales = [&](int blk) -> bool {
       if (!mbar_wait_warp(&sfull[j], jph, abort_flag, a.status)) return false;
-      const int t0 = w / mt * a.each, blk = (t0 + wg * hc) / Q_GROUP - t0 / Q_GROUP;
       const float* slot = slots + j * QR_SLOT;
       const float x = slot[row];
       s0 = x * slot[128 + blk];
@@ -539,10 +540,11 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     // Left at once when a wait fails: going on to the end of a loop from the
     // middle would keep both sides' sums alive, a select for each of them.
     auto run = [&]() {
-    if (walk0 < n_tiles && !scales(walk0)) return;
+    int blk = block_of(walk0);
+    if (walk0 < n_tiles && !scales(blk)) return;
     for (int w = walk0; w < n_tiles; w += n_walk) {
       const int t = (w % mt * CTAS + (int)rank) * 128 + row, n0 = w / mt * a.each + wg * hc;
-      const int edge = Q_GROUP - (n0 & (Q_GROUP - 1));
+      const int edge = Q_GROUP - (n0 & (Q_GROUP - 1)), blk_next = block_of(w + n_walk);
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
@@ -574,8 +576,8 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
         __syncwarp();
         if (lane == 0) mbar_arrive(&accfree[b]);
         add(112, vb);
-        const int w_next = kb + 1 < KB ? w : w + n_walk;
-        if (w_next < n_tiles && !scales(w_next)) return;
+        if (kb + 1 == KB) blk = blk_next;
+        if ((kb + 1 < KB || w + n_walk < n_tiles) && !scales(blk)) return;
         b ^= 1;
         if (!b) bph ^= 1;
       }
