@@ -330,20 +330,20 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 // ---------------------------------------------------------------- many tokens
 // Every block's sums (128 x 256 per CTA) pass from TMEM through registers, in
 // the time of the next block's four MMAs (512 cycles): 128 columns per thread,
-// 128 of its registers their sums, two pieces of 16 columns in flight (one
-// read while the other is multiplied).  384 threads leave 168 registers each.
+// 128 of its registers their sums (384 threads leave 168 each), multiplied and
+// added two at a time, since single multiply-adds alone would take the 512.
 constexpr int QR_EPI_WARPS = 8;
 constexpr int QR_PRODUCER = QR_EPI_WARPS, QR_SCALE = QR_EPI_WARPS + 1, QR_MMA = QR_EPI_WARPS + 2;   // + 3 idles
 constexpr int QR_THREADS = (QR_EPI_WARPS + 4) * 32;
-// Scales of a block: 128 tokens, up to 3 weight blocks.  Every token's come
+// Scales of two blocks: 128 tokens, up to 3 weight blocks.  Every token's come
 // from another line, with the latency of L2: 16 blocks of them are in flight.
-constexpr int QR_SLOTS = 16, QR_SLOT = 132;
+constexpr int QR_SLOTS = 8, QR_SLOT = 132;
 template <int CTAS>
 struct QrCfg {
   static constexpr int BN = 256;                        // weight rows per tile, at most
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / CTAS * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int FIXED = 1024 + 512 + QR_SLOTS * QR_SLOT * 4;
+  static constexpr int FIXED = 1024 + 512 + QR_SLOTS * 2 * QR_SLOT * 4;
   static constexpr int STAGES = (QL_SMEM - FIXED) / STAGE;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
 };
@@ -365,7 +365,7 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
   uint64_t* mma_done = sfree + QR_SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* slots = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE + 512);   // [QR_SLOTS][QR_SLOT]
+  float* slots = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE + 512);   // [QR_SLOTS][2][QR_SLOT]
   static_assert((2 * STAGES + 5 + 2 * QR_SLOTS) * 8 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -446,13 +446,17 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = a.xs + (size_t)min(m0 + i * 32 + lane, a.T - 1) * KB;
         const float* ws = a.Ws + (size_t)min(nb0 + min(lane, 2), nblk - 1) * KB;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = 0; kb < KB; kb += 2) {
           ok = mbar_wait_warp(&sfree[j], jph, abort_flag, a.status);   // the first round passes
           if (!ok) break;
-          float* slot = slots + j * QR_SLOT;
+          float* slot = slots + j * 2 * QR_SLOT;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) copy4_async(slot + i * 32 + lane, x[i] + kb, true);
-          if (lane < 3) copy4_async(slot + 128 + lane, ws + kb, true);
+          for (int q = 0; q < 2; ++q) {
+            const int k = min(kb + q, KB - 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) copy4_async(slot + q * QR_SLOT + i * 32 + lane, x[i] + k, true);
+            if (lane < 3) copy4_async(slot + q * QR_SLOT + 128 + lane, ws + k, true);
+          }
           copies_arrive(&sfull[j]);
           if (++j == QR_SLOTS) {
             j = 0;
@@ -519,16 +523,19 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(wg * hc);
     int b = 0, j = 0;
     uint32_t bph = 0, jph = 0;
-    float s0 = 0.0f, s1 = 0.0f;
+    float s0[2] = {0.0f, 0.0f}, s1[2] = {0.0f, 0.0f};
     // this half's first weight block, counted from the tile's first
     auto block_of = [&](int w) { return (w / mt * a.each + wg * hc) / Q_GROUP - w / mt * a.each / Q_GROUP; };
-    // the next block's scales, for a tile whose block_of is blk
+    // the next two blocks' scales, for a tile whose block_of is blk
     auto scales = [&](int blk) -> bool {
       if (!mbar_wait_warp(&sfull[j], jph, abort_flag, a.status)) return false;
-      const float* slot = slots + j * QR_SLOT;
-      const float x = slot[row];
-      s0 = x * slot[128 + blk];
-      s1 = x * slot[128 + min(blk + 1, 2)];
+      const float* slot = slots + j * 2 * QR_SLOT;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float x = slot[q * QR_SLOT + row];
+        s0[q] = x * slot[q * QR_SLOT + 128 + blk];
+        s1[q] = x * slot[q * QR_SLOT + 128 + min(blk + 1, 2)];
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sfree[j]);
       if (++j == QR_SLOTS) {
@@ -538,48 +545,44 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
       return true;
     };
     // Left at once when a wait fails: going on to the end of a loop from the
-    // middle would keep both sides' sums alive, a select for each of them.
+    // middle would keep both sides' sums alive.
     auto run = [&]() {
     int blk = block_of(walk0);
     if (walk0 < n_tiles && !scales(blk)) return;
     for (int w = walk0; w < n_tiles; w += n_walk) {
       const int t = (w % mt * CTAS + (int)rank) * 128 + row, n0 = w / mt * a.each + wg * hc;
       const int edge = Q_GROUP - (n0 & (Q_GROUP - 1)), blk_next = block_of(w + n_walk);
-      float acc[128];
+      uint64_t acc[64];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
       for (int kb = 0; kb < KB; ++kb) {
         if (!mbar_wait_warp(&accfull[b], bph, abort_flag, a.status)) return;
         tc_fence_after();
         const uint32_t src = tlane + (uint32_t)(b * BN);
-        const float u0 = s0, u1 = s1;
-        float va[16], vb[16];
-        auto add = [&](int c, const float (&v)[16]) {   // columns c .. c + 15; the edge is a multiple of 16
-          const float u = c < edge ? u0 : u1;
+        const uint64_t u0 = pack2(s0[0], s0[0]), u1 = pack2(s1[0], s1[0]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(v[i], u, acc[c + i]);
-        };
-        tmem_ask16(src, va);
-        tmem_have16(va);
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          tmem_ask16(src + c + 16, vb);
-          add(c, va);
-          tmem_have16(vb);
-          if (c < 96) {
-            tmem_ask16(src + c + 32, va);
-            add(c + 16, vb);
-            tmem_have16(va);
+        for (int c = 0; c < 128; c += 16) {   // the edge is a multiple of 16
+          uint64_t v[8];
+          tmem_get16x2(src + c, v);
+          if (c == 112) {   // all read: the next MMAs may have the columns
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&accfree[b]);
           }
+          const uint64_t u = c < edge ? u0 : u1;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[c / 2 + i] = fma2(v[i], u, acc[c / 2 + i]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&accfree[b]);
-        add(112, vb);
-        if (kb + 1 == KB) blk = blk_next;
-        if ((kb + 1 < KB || w + n_walk < n_tiles) && !scales(blk)) return;
         b ^= 1;
         if (!b) bph ^= 1;
+        s0[0] = s0[1];
+        s1[0] = s1[1];
+        if (kb + 1 == KB) blk = blk_next;
+        if ((kb & 1) && kb + 1 < KB) {
+          if (!scales(blk)) return;
+        } else if (kb + 1 == KB && w + n_walk < n_tiles) {
+          if (!scales(blk)) return;
+        }
       }
       const int cols = min(hc, a.n - n0);   // a multiple of 8
       if (t < a.T) {
@@ -588,7 +591,7 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
           if (c < cols) {
             float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = acc[c + i];
+            for (int i = 0; i < 4; ++i) unpack2(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
             const size_t at = ((size_t)t * a.n + n0 + c) / 8;
             if (a.y_f32) store8_f32(a.y, at, v);
             else store8_bf16(a.y, at, v);
