@@ -266,6 +266,19 @@ bool code_map(CUtensorMap* m, const void* base, long long inner, long long rows,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tensor map of an output [rows][cols], stored 64 bytes x 32 rows at a time.
+bool out_map(CUtensorMap* m, void* base, int f32, long long cols, long long rows) {
+  const EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * (f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {f32 ? 16u : 32u, 32u};
+  const cuuint32_t es[2] = {1u, 1u};
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN>
 cudaError_t qlinear_cols_attr() {
   return cudaFuncSetAttribute(k_qlinear_cols<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, QcCfg<BN>::SMEM);
@@ -297,7 +310,7 @@ sffn_status qlinear_rows(const sffn_qlinear_handle* h, const void* xq, QlinArgs 
   // columns per tile: what gives the least rounds x columns (a tile also costs
   // about 32 columns' time whatever its width)
   long long best = -1;
-  for (int n = 256; n >= 64; n -= 32) {
+  for (int n = 256; n >= 128; n -= 128) {
     const long long cost = ((mt * cdiv(a.n, n) + slots - 1) / slots) * (n + 32);
     if (best < 0 || cost < best) {
       best = cost;
@@ -306,10 +319,12 @@ sffn_status qlinear_rows(const sffn_qlinear_handle* h, const void* xq, QlinArgs 
   }
   const long long tiles = mt * cdiv(a.n, a.each);
   if (tiles > 0x7FFFFFFFll) return SFFN_ERR_UNSUPPORTED;
-  CUtensorMap mX, mW;
-  if (!code_map(&mX, xq, a.k, a.T, 128) || !code_map(&mW, h->desc.Wq, a.k, a.n, a.each / CTAS)) return SFFN_ERR_CUDA;
+  CUtensorMap mX, mW, mY;
+  if (!code_map(&mX, xq, a.k, a.T, 128) || !code_map(&mW, h->desc.Wq, a.k, a.n, a.each / CTAS) ||
+      !out_map(&mY, a.y, a.y_f32, a.n, a.T))
+    return SFFN_ERR_CUDA;
   return launched(launch_pdl(k_qlinear_rows<CTAS>, dim3((unsigned)std::min(tiles, slots) * CTAS), dim3(QR_THREADS),
-                             (size_t)QrCfg<CTAS>::SMEM, st, CTAS, mX, mW, a));
+                             (size_t)QrCfg<CTAS>::SMEM, st, CTAS, mX, mW, mY, a));
 }
 
 }  // namespace

@@ -107,6 +107,15 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, uint32
         : "memory");
 }
 
+// Tiled store from shared memory (a bulk group of the issuing thread); what
+// lies outside the map is not written.  c0 >= 0, c0 · element size a multiple of 16.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+
 template <int CTAS>
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
   if (CTAS == 2) {

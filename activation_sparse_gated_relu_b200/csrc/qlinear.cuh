@@ -335,28 +335,50 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 constexpr int QR_EPI_WARPS = 8;
 constexpr int QR_PRODUCER = QR_EPI_WARPS, QR_SCALE = QR_EPI_WARPS + 1, QR_MMA = QR_EPI_WARPS + 2;   // + 3 idles
 constexpr int QR_THREADS = (QR_EPI_WARPS + 4) * 32;
-// Scales of two blocks: 128 tokens, up to 3 weight blocks.  Every token's come
-// from another line, with the latency of L2: 16 blocks of them are in flight.
-constexpr int QR_SLOTS = 8, QR_SLOT = 132;
+// Scales of four blocks: 128 tokens' and 2 weight blocks', four values
+// each.  Every token's come from another line, with the latency of L2: 16
+// blocks of them are in flight.  The MMAs' operands and the copies that bring
+// them take most of shared memory's bandwidth, so a thread fetches four
+// blocks' scales with three loads.
+constexpr int QR_SLOTS = 4, QR_SLOT = 4 * 130;
+// y leaves through shared memory, 64 bytes of 32 rows per warp at a time, as
+// tiled copies: a thread's own stores (16 bytes of 32 rows each) took as long
+// as ten blocks of MMAs.
+constexpr int QR_OUT = 32 * 64;
 template <int CTAS>
 struct QrCfg {
   static constexpr int BN = 256;                        // weight rows per tile, at most
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / CTAS * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int FIXED = 1024 + 512 + QR_SLOTS * 2 * QR_SLOT * 4;
+  static constexpr int FIXED = 1024 + 512 + QR_SLOTS * QR_SLOT * 4 + QR_EPI_WARPS * QR_OUT;
   static constexpr int STAGES = (QL_SMEM - FIXED) / STAGE;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
 };
 
-// Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (a multiple of 32).
+// A warp's 32 rows of 64 bytes leave; rows and columns past the end are not written.
+__device__ __forceinline__ void store_rows(const CUtensorMap* map, const uint8_t* src, int col, int row) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (elect_one()) {
+    tma_store_2d(map, src, col, row);
+    bulk_commit();
+  }
+  __syncwarp();
+}
+
+// Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (128 or 256, so
+// that half of them lie in one weight block).
 template <int CTAS>
 __global__ void __launch_bounds__(QR_THREADS, 1)
-k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW, const QlinArgs a) {
+k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW,
+               const __grid_constant__ CUtensorMap mY, const QlinArgs a) {
   using Cfg = QrCfg<CTAS>;
   constexpr int STAGES = Cfg::STAGES, BN = Cfg::BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * Cfg::STAGE);
+  uint8_t* stage_out = smem + STAGES * Cfg::STAGE;                       // [QR_EPI_WARPS][QR_OUT]
+  float* slots = reinterpret_cast<float*>(stage_out + QR_EPI_WARPS * QR_OUT);   // [QR_SLOTS][QR_SLOT]
+  uint64_t* full = reinterpret_cast<uint64_t*>(slots + QR_SLOTS * QR_SLOT);
   uint64_t* empty = full + STAGES;
   uint64_t* accfull = empty + STAGES;   // [2]
   uint64_t* accfree = accfull + 2;      // [2]; the second CTA's epilogue signals its own, see the relay
@@ -365,7 +387,6 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
   uint64_t* mma_done = sfree + QR_SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* slots = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE + 512);   // [QR_SLOTS][2][QR_SLOT]
   static_assert((2 * STAGES + 5 + 2 * QR_SLOTS) * 8 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -445,17 +466,17 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
         const float* x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = a.xs + (size_t)min(m0 + i * 32 + lane, a.T - 1) * KB;
-        const float* ws = a.Ws + (size_t)min(nb0 + min(lane, 2), nblk - 1) * KB;
-        for (int kb = 0; kb < KB; kb += 2) {
+        const float* ws = a.Ws + (size_t)min(nb0 + (lane & 1), nblk - 1) * KB;
+        for (int kb = 0; kb < KB; kb += 4) {
           ok = mbar_wait_warp(&sfree[j], jph, abort_flag, a.status);   // the first round passes
           if (!ok) break;
-          float* slot = slots + j * 2 * QR_SLOT;
+          float* slot = slots + j * QR_SLOT;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 4; ++q) {
             const int k = min(kb + q, KB - 1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) copy4_async(slot + q * QR_SLOT + i * 32 + lane, x[i] + k, true);
-            if (lane < 3) copy4_async(slot + q * QR_SLOT + 128 + lane, ws + k, true);
+            for (int i = 0; i < 4; ++i) copy4_async(slot + (i * 32 + lane) * 4 + q, x[i] + k, true);
+            if (lane < 2) copy4_async(slot + (128 + lane) * 4 + q, ws + k, true);
           }
           copies_arrive(&sfull[j]);
           if (++j == QR_SLOTS) {
@@ -515,27 +536,21 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     __syncwarp();
   } else {
     // ------------------------------------------------------------- epilogue
-    // A thread has one token and half of the tile's columns, at most 128, which
-    // touch at most two weight blocks (the second from column `edge` on).
+    // A thread has one token and half of the tile's columns, at most 128.
     // Tiles narrower than 256 are read as if they were not: what the unused
     // columns hold is never stored, and a test would cost a select per sum.
     const int wg = warp >> 2, hc = a.each / 2, row = (warp & 3) * 32 + lane;
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(wg * hc);
     int b = 0, j = 0;
     uint32_t bph = 0, jph = 0;
-    float s0[2] = {0.0f, 0.0f}, s1[2] = {0.0f, 0.0f};
-    // this half's first weight block, counted from the tile's first
-    auto block_of = [&](int w) { return (w / mt * a.each + wg * hc) / Q_GROUP - w / mt * a.each / Q_GROUP; };
-    // the next two blocks' scales, for a tile whose block_of is blk
-    auto scales = [&](int blk) -> bool {
+    float sc[4];
+    const int blk = wg * hc / Q_GROUP;   // this half's weight block, counted from the tile's first
+    // the next four blocks' scales
+    auto scales = [&]() -> bool {
       if (!mbar_wait_warp(&sfull[j], jph, abort_flag, a.status)) return false;
-      const float* slot = slots + j * 2 * QR_SLOT;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float x = slot[q * QR_SLOT + row];
-        s0[q] = x * slot[q * QR_SLOT + 128 + blk];
-        s1[q] = x * slot[q * QR_SLOT + 128 + min(blk + 1, 2)];
-      }
+      const float4* slot = reinterpret_cast<const float4*>(slots + j * QR_SLOT);
+      const float4 x = slot[row], u = slot[128 + blk];
+      sc[0] = x.x * u.x, sc[1] = x.y * u.y, sc[2] = x.z * u.z, sc[3] = x.w * u.w;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sfree[j]);
       if (++j == QR_SLOTS) {
@@ -547,11 +562,9 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     // Left at once when a wait fails: going on to the end of a loop from the
     // middle would keep both sides' sums alive.
     auto run = [&]() {
-    int blk = block_of(walk0);
-    if (walk0 < n_tiles && !scales(blk)) return;
+    if (walk0 < n_tiles && !scales()) return;
     for (int w = walk0; w < n_tiles; w += n_walk) {
       const int t = (w % mt * CTAS + (int)rank) * 128 + row, n0 = w / mt * a.each + wg * hc;
-      const int edge = Q_GROUP - (n0 & (Q_GROUP - 1)), blk_next = block_of(w + n_walk);
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
@@ -559,9 +572,9 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
         if (!mbar_wait_warp(&accfull[b], bph, abort_flag, a.status)) return;
         tc_fence_after();
         const uint32_t src = tlane + (uint32_t)(b * BN);
-        const uint64_t u0 = pack2(s0[0], s0[0]), u1 = pack2(s1[0], s1[0]);
+        const uint64_t u = pack2(sc[0], sc[0]);
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {   // the edge is a multiple of 16
+        for (int c = 0; c < 128; c += 16) {
           uint64_t v[8];
           tmem_get16x2(src + c, v);
           if (c == 112) {   // all read: the next MMAs may have the columns
@@ -569,38 +582,56 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) mbar_arrive(&accfree[b]);
           }
-          const uint64_t u = c < edge ? u0 : u1;
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[c / 2 + i] = fma2(v[i], u, acc[c / 2 + i]);
         }
         b ^= 1;
         if (!b) bph ^= 1;
-        s0[0] = s0[1];
-        s1[0] = s1[1];
-        if (kb + 1 == KB) blk = blk_next;
-        if ((kb & 1) && kb + 1 < KB) {
-          if (!scales(blk)) return;
-        } else if (kb + 1 == KB && w + n_walk < n_tiles) {
-          if (!scales(blk)) return;
-        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q) sc[q] = sc[q + 1];
+        if (kb + 1 == KB ? w + n_walk < n_tiles : (kb & 3) == 3)
+          if (!scales()) return;
       }
-      const int cols = min(hc, a.n - n0);   // a multiple of 8
-      if (t < a.T) {
+      uint8_t* out = stage_out + warp * QR_OUT;
+      const int row0 = t - lane;
+      if (a.y_f32) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          if (c < cols) {
-            float v[8];
+        for (int c = 0; c < 128; c += 16) {
+          if (c < hc && n0 + c < a.n && row0 < a.T) {
+            if (elect_one()) bulk_wait_read();
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) unpack2(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
-            const size_t at = ((size_t)t * a.n + n0 + c) / 8;
-            if (a.y_f32) store8_f32(a.y, at, v);
-            else store8_bf16(a.y, at, v);
+            for (int i = 0; i < 4; ++i) {   // 16 bytes each, in the copy's 64-byte swizzle
+              float4 f;
+              unpack2(acc[c / 2 + 2 * i], f.x, f.y);
+              unpack2(acc[c / 2 + 2 * i + 1], f.z, f.w);
+              *reinterpret_cast<float4*>(out + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = f;
+            }
+            store_rows(&mY, out, n0 + c, row0);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          if (c < hc && n0 + c < a.n && row0 < a.T) {
+            if (elect_one()) bulk_wait_read();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float f[8];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) unpack2(acc[c / 2 + 4 * i + q], f[2 * q], f[2 * q + 1]);
+              store8_bf16(out + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16, 0, f);
+            }
+            store_rows(&mY, out, n0 + c, row0);
           }
         }
       }
     }
     };
     run();
+    __syncwarp();
+    if (elect_one()) bulk_wait_all();
   }
   __syncwarp();
   tc_fence_before();
