@@ -34,8 +34,8 @@ constexpr int GROUPED_MAX_E = 1024;
 constexpr int GT_EPI_WARPS = 8;                        // two warpgroups, every other 32 columns each
 constexpr int GT_PRODUCER = GT_EPI_WARPS;
 constexpr int GT_FIX = GT_EPI_WARPS + 1;              // clears what lies behind a group's end (weight gradient)
-constexpr int GT_MMA = GT_EPI_WARPS + 2;              // and the warp after it: half of a tile's columns each
-constexpr int GT_THREADS = (GT_EPI_WARPS + 4) * 32;
+constexpr int GT_MMA = GT_EPI_WARPS + 2;
+constexpr int GT_THREADS = (GT_EPI_WARPS + 3) * 32;
 constexpr int GT_BK = 64;                              // bf16 values of k per stage
 constexpr int GT_SMEM = 227 * 1024;
 
@@ -45,9 +45,7 @@ struct GtCfg {
   static constexpr int B_ROWS = BN / CTAS;             // columns whose operand a CTA holds
   static constexpr int A_BYTES = 128 * GT_BK * 2;
   static constexpr int B_BYTES = B_ROWS * GT_BK * 2;
-  // A CTA's columns of a tile's two halves lie HALF_OFF bytes apart, in boxes of BOX.
-  static constexpr int BOX = BN >= 128 ? 64 : 32;
-  static constexpr int HALF_OFF = B_BYTES / 2;
+  static constexpr int BOX = BN >= 128 ? 64 : 32;      // columns per copy
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int TABLE = (3 * (GROUPED_MAX_E + 1) * 4 + 127) & ~127;
   static constexpr int FIXED = 1024 /*align*/ + 384 /*barriers*/ + TABLE;
@@ -83,7 +81,6 @@ struct GtWalk {
   // the current tile
   int m0;                       // first row m of the tile (of the pair)
   int c0, cols, bn;             // first column, columns stored, columns computed
-  int bn0;                      // of them in the first half (the second may be empty)
   int krow;                     // weight gradient: first row of the group
   int kbs, ktail;               // k blocks, and values in the last one
   size_t orow;                  // output row of column 0
@@ -113,7 +110,6 @@ struct GtWalk {
       orow = (size_t)c0;
     }
     bn = (cols + STEP - 1) / STEP * STEP;
-    bn0 = BN >= 128 ? min(bn, BN / 2) : bn;
   }
 };
 
@@ -152,14 +148,14 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], CTAS);        // one arrival per CTA's producer
-      mbar_init(&empty[s], 2);          // both halves' MMAs have read it
+      mbar_init(&empty[s], 1);
       mbar_init(&tailbar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&accfull[b], 2);
+      mbar_init(&accfull[b], 1);
       mbar_init(&accfree[b], GT_EPI_WARPS * CTAS);
     }
-    mbar_init(mma_done, 2);
+    mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -213,11 +209,8 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
     for (int w = walk0; w < n_tiles && ok; w += n_walk) {
       t.set(w);
       const int m0 = t.m0 + (int)rank * 128;
-      // this CTA's columns of each half of the tile, boxes of BOX columns
-      const int p0 = t.bn0 / CTAS, p1 = (t.bn - t.bn0) / CTAS;
-      const int b0 = t.c0 + (int)rank * p0, b1 = t.c0 + t.bn0 + (int)rank * p1;
-      const int n0 = (p0 + BOX - 1) / BOX, n1 = (p1 + BOX - 1) / BOX;
-      const uint32_t bytes = Cfg::A_BYTES + (n0 + n1) * (BOX * GT_BK * 2);
+      const int half = t.bn / CTAS, b0 = t.c0 + (int)rank * half, nbox = (half + BOX - 1) / BOX;   // this CTA's columns
+      const uint32_t bytes = Cfg::A_BYTES + nbox * (BOX * GT_BK * 2);
       for (int kb = 0; kb < t.kbs; ++kb, ++it) {
         const int s = it % STAGES, f = it / STAGES;
         if (f > 0) ok = mbar_wait_warp(&empty[s], (f - 1) & 1, abort_flag, args.status);
@@ -241,11 +234,10 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
             tma_2d<CTAS>(sa, &mA, bar, m0, t.krow + k0);
             tma_2d<CTAS>(sa + 8192, &mA, bar, m0 + 64, t.krow + k0);
           }
-          for (int i = 0; i < n0 + n1; ++i) {
-            const int c = i < n0 ? b0 + BOX * i : b1 + BOX * (i - n0);
-            uint8_t* dst = sb + (i < n0 ? i * (BOX * GT_BK * 2) : Cfg::HALF_OFF + (i - n0) * (BOX * GT_BK * 2));
-            if (B_MN) tma_2d<CTAS>(dst, &mB, bar, c, t.krow + k0);
-            else tma_2d<CTAS>(dst, &mB, bar, k0, c);
+          for (int i = 0; i < nbox; ++i) {
+            uint8_t* dst = sb + i * (BOX * GT_BK * 2);
+            if (B_MN) tma_2d<CTAS>(dst, &mB, bar, b0 + BOX * i, t.krow + k0);
+            else tma_2d<CTAS>(dst, &mB, bar, k0, b0 + BOX * i);
           }
         }
       }
@@ -273,7 +265,7 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
       used ^= 1u << s;
       uint8_t* sa = smem + (size_t)s * Cfg::STAGE;
       uint8_t* sb = sa + Cfg::A_BYTES;
-      const int nbox = t.bn > t.bn0 ? 2 : 1;   // the halves, 64 columns each at most
+      const int nbox = (t.bn / CTAS + 63) / 64;
       const int k1 = (t.ktail + 15) & ~15;
       for (int i = lane; i < (k1 - t.ktail) * 8; i += 32) {
         const int at = t.ktail * 128 + i * 16;   // whole rows of 128 bytes: the swizzle permutes within a row
@@ -287,15 +279,11 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         else mbar_arrive(&full[s]);
       }
     }
-  } else if (warp >= GT_MMA) {
-    // ---------------------------------------------------------- MMA issuers
-    // One thread of each of two warps (of the pair's first CTA), a half of the
-    // columns each: an MMA's issue waits for the one before it, so what a
-    // thread does between its MMAs leaves the tensor core idle unless another
-    // thread's are there.
-    const int hf = warp - GT_MMA;
+  } else if (warp == GT_MMA) {
+    // ----------------------------------------------------------- MMA issuer
+    // One thread (of the pair's first CTA).
     if (rank == 0 && elect_one()) {
-      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + Cfg::A_BYTES + hf * Cfg::HALF_OFF;
+      const uint32_t sa0 = smem_u32(smem), sb0 = sa0 + Cfg::A_BYTES;
       const uint64_t ad0 = A_MN ? sdesc_mn_sw128(sa0, 8192) : sdesc_k_sw128(sa0);
       const uint64_t bd0 = B_MN ? sdesc_mn_sw128(sb0, 8192) : sdesc_k_sw128(sb0);
       constexpr uint32_t AK = A_MN ? 128u : 2u, BK = B_MN ? 128u : 2u;   // 16 values of k further
@@ -304,12 +292,11 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
       bool ok = true;
       for (int w = walk0; w < n_tiles && ok; w += n_walk) {
         t.set(w);
-        const int n = hf ? t.bn - t.bn0 : t.bn0;
-        const uint32_t idesc = idesc_bf16_f32(128 * CTAS, n) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16);
+        const uint32_t idesc = idesc_bf16_f32(128 * CTAS, t.bn) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16);
         for (int kc = 0; kc < t.kbs && ok; kc += args.kchunk) {
           ok = mbar_wait(&accfree[b], bph, abort_flag, args.status);
           if (!ok) break;
-          const uint32_t d = tmem + (uint32_t)(b * BN) + (hf ? t.bn0 : 0);
+          const uint32_t d = tmem + (uint32_t)(b * BN);
           const int k1 = min(kc + args.kchunk, t.kbs);
           for (int kb = kc; kb < k1; ++kb) {
             ok = mbar_wait(&full[s], ph, abort_flag, args.status);
@@ -317,11 +304,9 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
             tc_fence_after();
             const uint64_t ad = ad0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = bd0 + (uint32_t)(s * (Cfg::STAGE / 16));
             const int nk = kb == t.kbs - 1 ? (t.ktail + 15) / 16 : GT_BK / 16;
-            if (n > 0) {
 #pragma unroll
-              for (int k = 0; k < GT_BK / 16; ++k)
-                if (k < nk) pair_mma<CTAS, false>(d, ad + AK * k, bd + BK * k, idesc, (kb == kc && k == 0) ? 0u : 1u);
-            }
+            for (int k = 0; k < GT_BK / 16; ++k)
+              if (k < nk) pair_mma<CTAS, false>(d, ad + AK * k, bd + BK * k, idesc, (kb == kc && k == 0) ? 0u : 1u);
             pair_commit<CTAS>(&empty[s]);
             if (++s == STAGES) {
               s = 0;
@@ -340,80 +325,111 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
     // ------------------------------------------------------------- epilogue
     constexpr int NCH = (BN + 63) / 64;   // 32-column pieces per warpgroup
     const int wg = warp >> 2;
-    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (BN >= 64 ? 32u * wg : 0u);
     const uint32_t free0 = CTAS == 2 ? cluster_addr(smem_u32(&accfree[0]), 0) : smem_u32(&accfree[0]);
     int ci = 0;
-    // Left at once when a wait fails: leaving the inner loop from its middle
-    // would keep both sides' sums alive, a select for each of them.
-    auto run = [&]() {
-    for (int w = walk0; w < n_tiles; w += n_walk) {
-      t.set(w);
-      float acc[NCH][32];
-      for (int kc = 0; kc < t.kbs; kc += args.kchunk, ++ci) {
-        const int b = ci & 1;
-        if (!mbar_wait_warp(&accfull[b], (uint32_t)((ci >> 1) & 1), abort_flag, args.status)) return;
-        tc_fence_after();
-        // all of the tile's columns, computed or not: what the others hold is
-        // never stored, and a test would cost a select per value
-        const uint32_t at = tlane + (uint32_t)(b * BN + (BN >= 64 ? 32 * wg : 0));
-        if (kc == 0) {
+    // this warp has read accumulator b: the MMAs may refill it
+    auto release = [&](int b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CTAS == 2) mbar_arrive_cluster(free0 + 8 * b);
+        else mbar_arrive(&accfree[b]);
+      }
+    };
+    // columns c .. c + 31 of the tile, this thread's row m
+    auto store = [&](const float (&v)[32], int c) {
+      const int m = t.m0 + (int)rank * 128 + (warp & 3) * 32 + lane, n = t.cols - c;
+      if (m >= t.M) return;   // M is a multiple of 8: both lanes of a pair are in, or neither
+      if (args.out_f32) {
+        float* o = reinterpret_cast<float*>(args.out) + (t.orow + c) * (size_t)t.M + m;
+        if (n >= 32) {
 #pragma unroll
-          for (int j = 0; j < NCH; ++j) tmem_get32(at + 64u * j, acc[j]);
+          for (int i = 0; i < 32; ++i, o += t.M) *o = v[i];
         } else {
 #pragma unroll
-          for (int j = 0; j < NCH; ++j) {
+          for (int i = 0; i < 32; ++i, o += t.M)
+            if (i < n) *o = v[i];
+        }
+      } else {
+        // two columns at a time: even lanes store two rows m of the first one,
+        // odd lanes of the second
+        const int odd = lane & 1;
+        const uint32_t sel = odd ? 0x3276u : 0x5410u;
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(args.out) + (t.orow + c + odd) * (size_t)t.M + (m - odd);
+        const unsigned mask = __activemask();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2, o += 2 * (size_t)t.M) {
+          const uint32_t p = pack_bf16(v[i], v[i + 1]);
+          const uint32_t q = __shfl_xor_sync(mask, p, 1);
+          if (i + odd < n) *reinterpret_cast<uint32_t*>(o) = __byte_perm(p, q, sel);
+        }
+      }
+    };
+    // Left at once when a wait fails: leaving a loop from its middle would keep
+    // both sides' sums alive, a select for each of them.
+    auto run = [&]() {
+      for (int w = walk0; w < n_tiles; w += n_walk) {
+        t.set(w);
+        const int pieces = (t.cols - 32 * wg + 63) / 64;   // this warpgroup's, possibly none
+        if (t.kbs <= args.kchunk) {
+          // one sum in TMEM: from there to the output, a piece at a time
+          if (MODE == GROUPED_DW && t.kbs == 0) {
             float v[32];
-            tmem_get32(at + 64u * j, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[j][i] += v[i];
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (CTAS == 2) mbar_arrive_cluster(free0 + 8 * b);
-          else mbar_arrive(&accfree[b]);
-        }
-      }
-      if (MODE == GROUPED_DW && t.kbs == 0) {
-#pragma unroll
-        for (int j = 0; j < NCH; ++j)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[j][i] = 0.0f;
-      }
-      const int m = t.m0 + (int)rank * 128 + (warp & 3) * 32 + lane;
-      if (m < t.M) {   // M is a multiple of 8: both lanes of a pair are in, or neither
-#pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-          const int c = 64 * j + 32 * wg, n = t.cols - c;
-          if (n <= 0) break;
-          if (args.out_f32) {
-            float* o = reinterpret_cast<float*>(args.out) + (t.orow + c) * (size_t)t.M + m;
-            if (n >= 32) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i, o += t.M) *o = acc[j][i];
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i, o += t.M)
-                if (i < n) *o = acc[j][i];
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+#pragma unroll 1
+            for (int j = 0; j < pieces; ++j) {
+              store(v, 64 * j + 32 * wg);
+              __syncwarp();
             }
-          } else {
-            // two columns at a time: even lanes store two rows m of the first
-            // one, odd lanes of the second
-            const int odd = lane & 1;
-            const uint32_t sel = odd ? 0x3276u : 0x5410u;
-            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(args.out) + (t.orow + c + odd) * (size_t)t.M + (m - odd);
-            const unsigned mask = __activemask();
-#pragma unroll
-            for (int i = 0; i < 32; i += 2, o += 2 * (size_t)t.M) {
-              const uint32_t p = pack_bf16(acc[j][i], acc[j][i + 1]);
-              const uint32_t q = __shfl_xor_sync(mask, p, 1);
-              if (i + odd < n) *reinterpret_cast<uint32_t*>(o) = __byte_perm(p, q, sel);
-            }
+            continue;
           }
+          const int b = ci & 1;
+          if (!mbar_wait_warp(&accfull[b], (uint32_t)((ci >> 1) & 1), abort_flag, args.status)) return;
+          ++ci;
+          tc_fence_after();
+          if (pieces <= 0) release(b);
+#pragma unroll 1
+          for (int j = 0; j < pieces; ++j) {
+            float v[32];
+            tmem_get32(tlane + (uint32_t)(b * BN + 64 * j), v);
+            if (j == pieces - 1) release(b);
+            store(v, 64 * j + 32 * wg);
+            __syncwarp();
+          }
+        } else {
+          // several: added up in registers, all of the tile's columns, computed
+          // or not (what the others hold is never stored, and a test would cost
+          // a select per value)
+          float acc[NCH][32];
+#pragma unroll
+          for (int j = 0; j < NCH; ++j)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[j][i] = 0.0f;
+          for (int kc = 0; kc < t.kbs; kc += args.kchunk, ++ci) {
+            const int b = ci & 1;
+            if (!mbar_wait_warp(&accfull[b], (uint32_t)((ci >> 1) & 1), abort_flag, args.status)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < NCH; ++j)
+#pragma unroll
+              for (int h = 0; h < 32; h += 16) {
+                float v[16];
+                tmem_get16(tlane + (uint32_t)(b * BN + 64 * j + h), v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[j][h + i] += v[i];
+              }
+            release(b);
+          }
+#pragma unroll
+          for (int j = 0; j < NCH; ++j)
+            if (j < pieces) {
+              store(acc[j], 64 * j + 32 * wg);
+              __syncwarp();
+            }
         }
       }
-    }
     };
     run();
   }
