@@ -73,6 +73,23 @@ __device__ __forceinline__ bool group_rows(const int* off, int e, int R, int* a,
   return u >= 0 && v >= u && v <= R;
 }
 
+// a / b and the remainder, a >= 0, b > 0.  Every role of a CTA does this between
+// two tiles; an integer division there takes several times as long.
+__device__ __forceinline__ int div_rem(int a, int b, int* rem) {
+  int q = (int)((float)a * __frcp_rn((float)b));   // off by one step or two at most for a / b < 2^21
+  int r = a - q * b;
+  while (r < 0) {
+    --q;
+    r += b;
+  }
+  while (r >= b) {
+    ++q;
+    r -= b;
+  }
+  *rem = r;
+  return q;
+}
+
 // The tiles of all experts in order, one role's walk over them.
 template <int MODE, int CTAS, int BN>
 struct GtWalk {
@@ -91,8 +108,9 @@ struct GtWalk {
     constexpr int STEP = 16 * CTAS;
     if (MODE == GROUPED_DW) {
       const int nt = (N + BN - 1) / BN;
-      m0 = t / nt * (128 * CTAS);
-      c0 = t % nt * BN;
+      int j;
+      m0 = div_rem(t, nt, &j) * (128 * CTAS);
+      c0 = j * BN;
       cols = min(BN, N - c0);
       krow = a;
       kbs = (rows + GT_BK - 1) / GT_BK;
@@ -101,9 +119,10 @@ struct GtWalk {
     } else {
       // the fewest tiles of at most BN columns, even ones
       const int nt = (rows + BN - 1) / BN;
-      const int each = ((rows + nt - 1) / nt + STEP - 1) / STEP * STEP;
-      m0 = t / nt * (128 * CTAS);
-      c0 = a + t % nt * each;
+      int j;
+      const int each = (div_rem(rows + nt - 1, nt, &j) + STEP - 1) / STEP * STEP;
+      m0 = div_rem(t, nt, &j) * (128 * CTAS);
+      c0 = a + j * each;
       cols = min(each, a + rows - c0);
       kbs = (K + GT_BK - 1) / GT_BK;
       ktail = K - (kbs - 1) * GT_BK;
