@@ -123,13 +123,25 @@ cudaError_t norm_launch_res(int res, int out, const NormArgs& a, const NormShape
                     : norm_launch_out<XF32, 2>(out, a, s, st);
 }
 
+template <bool SF32, bool DYF32, bool DS, int NV>
+cudaError_t norm_bwd_launch_nv(const NormBwdArgs& a, const NormShape& s, int ctas, cudaStream_t st) {
+  const int smem = NormBwdCfg<SF32, DYF32, DS, NV>::smem(s.threads);
+  const auto kernel = k_rmsnorm_bwd<SF32, DYF32, DS, NV>;
+  // set on every call: it belongs to the current device, and costs little
+  const cudaError_t e =
+      smem > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
+  if (e) {
+    cudaGetLastError();
+    return e;
+  }
+  return launch_pdl(kernel, dim3(ctas), dim3(s.threads), (size_t)smem, st, 1, a);
+}
 template <bool SF32, bool DYF32, bool DS>
 cudaError_t norm_bwd_launch(const NormBwdArgs& a, const NormShape& s, int ctas, cudaStream_t st) {
-  const dim3 grid(ctas), block(s.threads);
   switch (s.nv) {
-    case 1: return launch_pdl(k_rmsnorm_bwd<SF32, DYF32, DS, 1>, grid, block, 0, st, 1, a);
-    case 2: return launch_pdl(k_rmsnorm_bwd<SF32, DYF32, DS, 2>, grid, block, 0, st, 1, a);
-    default: return launch_pdl(k_rmsnorm_bwd<SF32, DYF32, DS, 4>, grid, block, 0, st, 1, a);
+    case 1: return norm_bwd_launch_nv<SF32, DYF32, DS, 1>(a, s, ctas, st);
+    case 2: return norm_bwd_launch_nv<SF32, DYF32, DS, 2>(a, s, ctas, st);
+    default: return norm_bwd_launch_nv<SF32, DYF32, DS, 4>(a, s, ctas, st);
   }
 }
 template <bool SF32, bool DYF32>
@@ -210,7 +222,7 @@ extern "C" sffn_status sffn_rmsnorm_backward(const sffn_rmsnorm_desc* desc, cons
            : (yf ? norm_bwd_launch_ds<false, true>(a, s, ctas, st) : norm_bwd_launch_ds<false, false>(a, s, ctas, st));
   }
   e = e ? e
-        : launch_pdl(k_rmsnorm_dw, dim3(cdiv(desc->d, 32)), dim3(256), 0, st, 1, (const float*)workspace, ctas * s.rpc,
+        : launch_pdl(k_rmsnorm_dw, dim3(cdiv(desc->d, 32)), dim3(512), 0, st, 1, (const float*)workspace, ctas * s.rpc,
                      desc->d, dweight);
   return launched(e);
 }

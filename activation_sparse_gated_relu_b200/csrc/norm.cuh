@@ -17,6 +17,7 @@
 // threads share a CTA.  Sums are fp32, in a fixed order.
 #pragma once
 
+#include "ptx_pair.cuh"
 #include "vec8.cuh"
 
 namespace sffn {
@@ -46,8 +47,8 @@ __device__ __forceinline__ void load_w8(const void* w, int w_f32, int vec, float
   }
 }
 
-// Sums of v[0..N) over the row's threads: warp sums to shared memory, then
-// every thread adds its row's warps in order.
+// Sums of v[0..N) over the row's threads (the same in all of them): warp sums to
+// shared memory, then every warp adds its row's, a power of two, in pairs.
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[16], int warps_per_row) {
 #pragma unroll
@@ -60,13 +61,12 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[16], int war
 #pragma unroll
     for (int i = 0; i < N; ++i) red[i][warp] = v[i];
   __syncthreads();
-  const int w0 = warp / warps_per_row * warps_per_row;
+  const int lane = threadIdx.x & 31, w = warp / warps_per_row * warps_per_row + (lane & (warps_per_row - 1));
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float t = 0.0f;
-    for (int k = 0; k < warps_per_row; ++k) t += red[i][w0 + k];
-    v[i] = t;
-  }
+  for (int i = 0; i < N; ++i) v[i] = red[i][w];
+  for (int o = warps_per_row >> 1; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
 }
 
 // RES: 0 none, 1 bf16, 2 fp32.  OUT: 0 bf16, 1 fp32, 2 e4m3 with scales.
@@ -139,101 +139,188 @@ struct NormBwdArgs {
   float eps;
 };
 
+// A row is a chain (load, two sums over its threads, gradient), so several
+// rows' values are on their way while one is worked on: every thread copies
+// its own eight columns of the rows to come into shared memory, STAGES rows
+// ahead, and reads them back itself, without any barrier.  Two CTAs an SM.
+// Where the rows are too wide for that (d > 8192 in fp32), STAGES is 0 and
+// they are loaded as they are needed.  What is left is bound by instruction
+// issue, so the arithmetic runs on pairs of columns.
+template <bool SF32, bool DYF32, bool DS, int NV>
+struct NormBwdCfg {
+  static constexpr int NS = SF32 ? 2 : 1, NY = DYF32 ? 2 : 1, ND = DS ? NS : 0;
+  static constexpr int PER = (NS + NY + ND) * NV;              // 16-byte pieces per thread and row
+  static constexpr int STAGES = PER <= 3 ? 4 : PER <= 6 ? 4 : PER <= 12 ? 2 : 0;
+  static constexpr int smem(int threads) { return STAGES * PER * 16 * threads; }
+};
+
 // One group of threads takes rows g, g + groups, ... and keeps its part of dw
 // in registers over them.
 template <bool SF32, bool DYF32, bool DS, int NV>
-__global__ void __launch_bounds__(512) k_rmsnorm_bwd(const NormBwdArgs a) {
+__global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) k_rmsnorm_bwd(const NormBwdArgs a) {
+  using Cfg = NormBwdCfg<SF32, DYF32, DS, NV>;
+  constexpr int STAGES = Cfg::STAGES, NS = Cfg::NS, NY = Cfg::NY, ND = Cfg::ND;
   __shared__ float red[2][2][16];
+  extern __shared__ uint4 ring[];      // [STAGES][PER][threads]
   const int tid = threadIdx.x & (a.tpr - 1);
   const int dv = a.d / 8;
   const int rpc = blockDim.x / a.tpr;
   const long long g = (long long)blockIdx.x * rpc + threadIdx.x / a.tpr;
+  const long long step = (long long)gridDim.x * rpc;
   griddep_wait();
-  float w[NV][8], dw[NV][8];
+  uint64_t dw[NV][4];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[i][j] = 0;
+  // with eight columns per thread the weight stays in registers
+  uint64_t w1[4];
+  auto weight = [&](int i, uint64_t (&f)[4]) {
     const int v = tid + i * a.tpr;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (v < dv) load_w8(a.w, a.w_f32, v, x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.0f;
-    if (v < dv) load_w8(a.w, a.w_f32, v, w[i]);
-  }
-  int par = 0;
-  for (long long t0 = (long long)blockIdx.x * rpc; t0 < a.T; t0 += (long long)gridDim.x * rpc, par ^= 1) {
+    for (int j = 0; j < 4; ++j) f[j] = pack2(x[2 * j], x[2 * j + 1]);
+  };
+  if (NV == 1) weight(0, w1);
+  // this thread's pieces of the next row to ask for, row t, into ring slot
+  // `slot` (zeros past the end)
+  long long at_ask = g * dv + tid;
+  auto ask = [&](long long t, int slot) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = t < a.T && tid + i * a.tpr < dv;
+      const long long at = in ? at_ask + i * a.tpr : 0;
+      uint4* to = ring + ((size_t)slot * Cfg::PER + i * (NS + NY + ND)) * blockDim.x + threadIdx.x;
+#pragma unroll
+      for (int k = 0; k < NS; ++k) copy16_async(to + k * blockDim.x, reinterpret_cast<const uint4*>(a.s) + at * NS + k, in);
+#pragma unroll
+      for (int k = 0; k < NY; ++k)
+        copy16_async(to + (NS + k) * blockDim.x, reinterpret_cast<const uint4*>(a.dy) + at * NY + k, in);
+#pragma unroll
+      for (int k = 0; k < ND; ++k)
+        copy16_async(to + (NS + NY + k) * blockDim.x, reinterpret_cast<const uint4*>(a.ds) + at * NS + k, in);
+    }
+    at_ask += step * dv;
+    copies_commit();
+  };
+#pragma unroll
+  for (int q = 0; q < (STAGES > 0 ? STAGES - 1 : 0); ++q) ask(g + q * step, q);
+  int par = 0, slot = 0;
+  long long at_row = g * dv + tid;
+  for (long long t0 = (long long)blockIdx.x * rpc; t0 < a.T; t0 += step, par ^= 1, at_row += step * dv) {
     const long long t = t0 + threadIdx.x / a.tpr;
     const bool row = t < a.T;
     Raw8<SF32> rs[NV], rd[NV];
     Raw8<DYF32> ry[NV];
+    if (STAGES > 0) {
+      ask(t + (STAGES - 1) * step, (slot + STAGES - 1) & (STAGES > 0 ? STAGES - 1 : 0));
+      copies_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = tid + i * a.tpr;
-      rs[i].zero();
-      ry[i].zero();
-      rd[i].zero();
-      if (row && v < dv) {
-        rs[i].load(a.s, (size_t)t * dv + v);
-        ry[i].load(a.dy, (size_t)t * dv + v);
-        if (DS) rd[i].load(a.ds, (size_t)t * dv + v);
+      if (STAGES > 0) {
+        const uint4* from = ring + ((size_t)slot * Cfg::PER + i * (NS + NY + ND)) * blockDim.x + threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < NS; ++k) rs[i].v[k] = from[k * blockDim.x];
+#pragma unroll
+        for (int k = 0; k < NY; ++k) ry[i].v[k] = from[(NS + k) * blockDim.x];
+#pragma unroll
+        for (int k = 0; k < ND; ++k) rd[i].v[k] = from[(NS + NY + k) * blockDim.x];
+      } else {
+        rs[i].zero();
+        ry[i].zero();
+        rd[i].zero();
+        if (row && tid + i * a.tpr < dv) {
+          rs[i].load(a.s, at_row + i * a.tpr);
+          ry[i].load(a.dy, at_row + i * a.tpr);
+          if (DS) rd[i].load(a.ds, at_row + i * a.tpr);
+        }
       }
     }
-    float sum[2] = {0.0f, 0.0f};
+    if (STAGES > 0) slot = (slot + 1) & (STAGES - 1);
+    uint64_t s0 = 0, s1 = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float s[8], y[8];
-      rs[i].get(s);
-      ry[i].get(y);
+      uint64_t s[4], y[4], w[4];
+      rs[i].pairs(s);
+      ry[i].pairs(y);
+      if (NV > 1) weight(i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sum[0] += s[j] * s[j];
-        sum[1] += s[j] * (y[j] * w[i][j]);
+      for (int j = 0; j < 4; ++j) {
+        s0 = fma2(s[j], s[j], s0);
+        s1 = fma2(s[j], mul2(y[j], NV == 1 ? w1[j] : w[j]), s1);
       }
     }
+    float sum[2], hi;
+    unpack2(s0, sum[0], hi);
+    sum[0] += hi;
+    unpack2(s1, sum[1], hi);
+    sum[1] += hi;
     row_sum<2>(sum, red[par], a.tpr >> 5);
     const float rstd = rsqrtf(sum[0] / (float)a.d + a.eps);
     const float c = sum[1] * rstd * rstd * rstd / (float)a.d;
+    const uint64_t r2 = pack2(rstd, rstd), c2 = pack2(-c, -c);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = tid + i * a.tpr;
-      float s[8], y[8], dx[8];
-      rs[i].get(s);
-      ry[i].get(y);
+      uint64_t s[4], y[4], w[4], dx[4];
+      rs[i].pairs(s);
+      ry[i].pairs(y);
+      if (NV > 1) weight(i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        dx[j] = rstd * (y[j] * w[i][j]) - s[j] * c;
-        if (row) dw[i][j] += y[j] * (s[j] * rstd);
+      for (int j = 0; j < 4; ++j) {
+        dx[j] = fma2(s[j], c2, mul2(mul2(y[j], NV == 1 ? w1[j] : w[j]), r2));
+        dw[i][j] = fma2(y[j], mul2(s[j], r2), dw[i][j]);   // rows past the end are zeros
       }
       if (DS) {
-        rd[i].get(s);
+        rd[i].pairs(s);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dx[j] += s[j];
+        for (int j = 0; j < 4; ++j) dx[j] = add2(dx[j], s[j]);
       }
-      if (row && v < dv) {
-        if (SF32) store8_f32(a.dx, (size_t)t * dv + v, dx);
-        else store8_bf16(a.dx, (size_t)t * dv + v, dx);
+      if (row && tid + i * a.tpr < dv) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) unpack2(dx[j], f[2 * j], f[2 * j + 1]);
+        if (SF32) store8_f32(a.dx, at_row + i * a.tpr, f);
+        else store8_bf16(a.dx, at_row + i * a.tpr, f);
       }
     }
   }
+  if (STAGES > 0) copies_wait<0>();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = tid + i * a.tpr;
-    if (v < dv) store8_f32(a.part, (size_t)g * dv + v, dw[i]);
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpack2(dw[i][j], f[2 * j], f[2 * j + 1]);
+    if (v < dv) store8_f32(a.part, (size_t)g * dv + v, f);
   }
 }
 
-// dw[c] = sum over the n_part partial rows, eight warps taking every eighth
-// row and added in order.  One CTA per 32 columns.
-__global__ void __launch_bounds__(256) k_rmsnorm_dw(const float* part, int n_part, int d, float* dw) {
-  __shared__ float red[8][32];
+// dw[c] = sum over the n_part partial rows, sixteen warps taking every
+// sixteenth row and added in order.  One CTA per 32 columns.
+__global__ void __launch_bounds__(512) k_rmsnorm_dw(const float* part, int n_part, int d, float* dw) {
+  __shared__ float red[16][32];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
   griddep_wait();
   float t = 0.0f;
-  if (c < d)
-    for (int p = k; p < n_part; p += 8) t += part[(size_t)p * d + c];
+  if (c < d) {
+    int p = k;
+    for (; p + 112 < n_part; p += 128) {   // eight loads in flight, added in order
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = part[(size_t)(p + 16 * i) * d + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += v[i];
+    }
+    for (; p < n_part; p += 16) t += part[(size_t)p * d + c];
+  }
   red[k][threadIdx.x & 31] = t;
   __syncthreads();
   if (k == 0 && c < d) {
     float u = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u += red[i][threadIdx.x];
+    for (int i = 0; i < 16; ++i) u += red[i][threadIdx.x];
     dw[c] = u;
   }
 }

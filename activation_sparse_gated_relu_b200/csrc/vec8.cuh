@@ -4,7 +4,7 @@
 
 #include <cuda_fp8.h>
 
-#include "ptx.cuh"
+#include "ptx_pair.cuh"
 
 namespace sffn {
 
@@ -26,6 +26,19 @@ struct Raw8 {
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < (F32 ? 2 : 1); ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void pairs(uint64_t (&f)[4]) const {
+    if (F32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[2 * i] = pack2(__uint_as_float(v[F32 ? i : 0].x), __uint_as_float(v[F32 ? i : 0].y));
+        f[2 * i + 1] = pack2(__uint_as_float(v[F32 ? i : 0].z), __uint_as_float(v[F32 ? i : 0].w));
+      }
+    } else {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = pack2(bf16lo(w[i]), bf16hi(w[i]));
+    }
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     if (F32) {

@@ -21,6 +21,7 @@ GROUP = 128     # columns that share a scale, and the side of a weight block tha
 _BF16, _FP32, _FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 _CODE = {_BF16: SFFN_BF16, _FP32: SFFN_FP32, _FP8: SFFN_E4M3}
 _OUT = {"bf16": _BF16, "fp32": _FP32}
+_VALUES = (_BF16, _FP32)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -148,6 +149,7 @@ class RmsNorm:
         ptr = _check(weight, "weight", (_BF16, _FP32), (self.d,), None)
         self.weight, self.eps, self.device = weight, float(eps), weight.get_device()
         self._lib = load_library()
+        self._call = self._lib.sffn_rmsnorm_forward
         self._desc = {}
         # refuse a size or an eps here rather than at the first call
         n = ctypes.c_size_t()
@@ -169,43 +171,51 @@ class RmsNorm:
         T, d = _matrix(x, "x")
         dev = self.device
         shape = (T, self.d)
-        xp = _check(x, "x", (_BF16, _FP32), shape, dev)
+        xp = _check(x, "x", _VALUES, shape, dev)
         rp = sp = cp = None
+        rt = _BF16
         if residual is not None:
-            rp = _check(residual, "residual", (_BF16, _FP32), shape, dev)
+            rp = _check(residual, "residual", _VALUES, shape, dev)
+            rt = residual.dtype
         elif residual_out is not None:
             raise ValueError("residual_out needs a residual")
+        given = y is not None or scale is not None or residual_out is not None
         with _where(dev, stream):
-            made = []
             if y is None:
-                y = torch.empty(shape, dtype=dtype, device=x.device)
-                yp = y.data_ptr()
-            else:
-                yp = _check(y, "y", (dtype,), shape, dev)
-                made.append((y, "y"))
-            if residual is not None:
-                if residual_out is None:
-                    residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
-                    sp = residual_out.data_ptr()
-                else:
-                    sp = _check(residual_out, "residual_out", (residual.dtype,), shape, dev)
-                    made.append((residual_out, "residual_out"))
+                y = torch.empty_like(x, dtype=dtype)
+            if residual is not None and residual_out is None:
+                residual_out = torch.empty_like(residual)
+            if dtype is _FP8 and scale is None:
+                scale = x.new_empty((T, _groups(d)), dtype=_FP32)
+            if given:
+                self._check_outputs(x, residual, dtype, y, scale, residual_out, shape)
+            yp = y.data_ptr()
+            if rp is not None:
+                sp = residual_out.data_ptr()
             if dtype is _FP8:
-                if scale is None:
-                    scale = torch.empty((T, _groups(d)), dtype=_FP32, device=x.device)
-                    cp = scale.data_ptr()
-                else:
-                    cp = _check(scale, "scale", (_FP32,), (T, _groups(d)), dev)
-                    made.append((scale, "scale"))
-            for i, (t, name) in enumerate(made):
-                if name == "scale":
-                    _apart(t, name, x, *(() if residual is None else (residual,)))
-                else:
-                    _apart_or_in_place(t, name, x, residual)
-                _apart(t, name, self.weight, *(u for u, _ in made[:i]))
-            desc = self._descriptor(x.dtype, residual.dtype if residual is not None else _BF16, dtype)
-            _ok(self._lib.sffn_rmsnorm_forward(desc, xp, rp, T, sp, yp, cp, _raw_stream(dev)), "RmsNorm.forward")
+                cp = scale.data_ptr()
+            s = self._call(self._descriptor(x.dtype, rt, dtype), xp, rp, T, sp, yp, cp, _raw_stream(dev))
+            if s:
+                raise SffnError(s, "RmsNorm.forward")
         return y, scale, residual_out if residual is not None else x
+
+    def _check_outputs(self, x, residual, dtype, y, scale, residual_out, shape) -> None:
+        """Outputs that the caller gave (or that were made beside them)."""
+        dev = self.device
+        _check(y, "y", (dtype,), shape, dev)
+        made = [(y, "y")]
+        if residual is not None:
+            _check(residual_out, "residual_out", (residual.dtype,), shape, dev)
+            made.append((residual_out, "residual_out"))
+        if dtype is _FP8:
+            _check(scale, "scale", (_FP32,), (shape[0], _groups(self.d)), dev)
+            made.append((scale, "scale"))
+        for i, (t, name) in enumerate(made):
+            if name == "scale":
+                _apart(t, name, x, *(() if residual is None else (residual,)))
+            else:
+                _apart_or_in_place(t, name, x, residual)
+            _apart(t, name, self.weight, *(u for u, _ in made[:i]))
 
     def forward(self, x, residual=None, *, out: str = "bf16", y=None, residual_out=None, stream: Optional[int] = None):
         """(y, s): x [T][d] bf16 or fp32, residual [T][d] bf16 or fp32 or None,
@@ -261,9 +271,9 @@ def quantize_rows(x, *, codes=None, scale=None, stream: Optional[int] = None):
     xp = _check(x, "x", (_BF16, _FP32), (T, d), dev)
     with _where(dev, stream):
         if codes is None:
-            codes = torch.empty((T, d), dtype=_FP8, device=x.device)
+            codes = torch.empty_like(x, dtype=_FP8)
         if scale is None:
-            scale = torch.empty((T, _groups(d)), dtype=_FP32, device=x.device)
+            scale = x.new_empty((T, _groups(d)), dtype=_FP32)
         qp = _check(codes, "codes", (_FP8,), (T, d), dev)
         cp = _check(scale, "scale", (_FP32,), (T, _groups(d)), dev)
         _ok(load_library().sffn_quantize_rows(xp, _CODE[x.dtype], T, d, qp, cp, _raw_stream(dev)), "quantize_rows")
@@ -354,7 +364,7 @@ class Fp8Linear(_Handle):
                 q, scale = quantize_rows(x)
                 xp, cp = q.data_ptr(), scale.data_ptr()
             if y is None:
-                y = torch.empty((T, self.d_out), dtype=dtype, device=x.device)
+                y = x.new_empty((T, self.d_out), dtype=dtype)
                 yp = y.data_ptr()
             else:
                 yp = _check(y, "y", (dtype,), (T, self.d_out), dev)
@@ -408,7 +418,7 @@ class GroupedLinear(_Handle):
         dev = self.device
         with _where(dev, stream):
             if y is None:
-                y = torch.empty((R, self.d_out), dtype=dtype, device=x.device)
+                y = x.new_empty((R, self.d_out), dtype=dtype)
                 yp = y.data_ptr()
             else:
                 yp = _check(y, "y", (dtype,), (R, self.d_out), dev)
@@ -429,14 +439,14 @@ class GroupedLinear(_Handle):
         yp = _check(dy, "dy", (_BF16,), (R, self.d_out), dev)
         with _where(dev, stream):
             if dx is None:
-                dx = torch.empty((R, self.d_in), dtype=dtype, device=x.device)
+                dx = torch.empty_like(x, dtype=dtype)
                 gp = dx.data_ptr()
             else:
                 gp = _check(dx, "dx", (dtype,), (R, self.d_in), dev)
                 _apart(dx, "dx", x, dy, self.W, offsets)
             shape = (self.n_experts, self.d_out, self.d_in)
             if dW is None:
-                dW = torch.empty(shape, dtype=_FP32, device=x.device)
+                dW = torch.empty_like(self.W, dtype=_FP32)
                 wp = dW.data_ptr()
             else:
                 wp = _check(dW, "dW", (_FP32, _BF16), shape, dev)
