@@ -170,6 +170,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sffn_quantize_blocks.argtypes = [vp, ip, ip, ip, vp, vp, vp]
     lib.sffn_qlinear_create.argtypes = [ctypes.POINTER(sffn_qlinear_desc), vp, ctypes.POINTER(vp)]
     lib.sffn_qlinear_forward.argtypes = [vp, vp, vp, ip, vp, ip, vp]
+    lib.sffn_qlinear_quantize_forward.argtypes = [vp, vp, ip, ip, vp, ip, vp, sz, vp]
     lib.sffn_qlinear_read_status.argtypes = [vp, vp]
     lib.sffn_qlinear_destroy.argtypes = [vp]
     lib.sffn_grouped_create.argtypes = [ctypes.POINTER(sffn_grouped_desc), vp, ctypes.POINTER(vp)]
@@ -179,8 +180,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sffn_grouped_read_status.argtypes = [vp, vp]
     lib.sffn_grouped_destroy.argtypes = [vp]
     for fn in ("rmsnorm_forward", "rmsnorm_backward", "rmsnorm_workspace_bytes", "quantize_rows", "quantize_blocks",
-               "qlinear_create", "qlinear_forward", "qlinear_read_status", "qlinear_destroy", "grouped_create",
-               "grouped_forward", "grouped_backward_input", "grouped_backward_weight", "grouped_read_status",
+               "qlinear_create", "qlinear_forward", "qlinear_quantize_forward", "qlinear_read_status",
+               "qlinear_destroy", "grouped_create", "grouped_forward", "grouped_backward_input", "grouped_backward_weight", "grouped_read_status",
                "grouped_destroy"):
         getattr(lib, "sffn_" + fn).restype = st
     lib.sffn_version.argtypes = []

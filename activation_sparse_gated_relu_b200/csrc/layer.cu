@@ -260,6 +260,7 @@ extern "C" sffn_status sffn_quantize_blocks(const void* W, sffn_dtype w_dtype, i
 struct sffn_qlinear_handle {
   sffn_qlinear_desc desc;
   int dev = 0, n_sm = 0;
+  int slots[4] = {0, 0, 0, 0};  // clusters of 1, 2, 4 and 8 CTAs that the GPU holds at once, one CTA per SM
   uint32_t* status = nullptr;   // [4]
 };
 
@@ -299,12 +300,26 @@ cudaError_t qlinear_cols_attr() {
 template <int BN>
 sffn_status qlinear_cols(const sffn_qlinear_handle* h, const void* xq, QlinArgs a, cudaStream_t st) {
   a.each = cdiv(a.T, 16) * 16;
-  // One tile per SM: tiles of 128 weight rows, cut along k over up to 8 CTAs
-  // where they leave SMs idle, then rows per tile evened out over what is left.
-  const int nt = cdiv(a.n, 128);
-  a.split = 1;
-  while (a.split < 8 && nt * a.split * 2 <= h->n_sm && a.kb >= 8 * a.split) a.split *= 2;
-  a.h = std::min(128, std::max(8, cdiv(cdiv((long long)a.n * a.split, h->n_sm), 8) * 8));
+  // How many CTAs share a tile's k, and how many weight rows a tile has: the
+  // least time by a model of it, in cycles.  Every cluster that fits gets one
+  // tile of even height, or several.  A block of k costs its bytes at 25 per
+  // cycle and SM (the SMs' share of the memory bandwidth), and no less than its
+  // four MMAs, 200; a sum over a cluster costs 3000.  Measured at 13 tokens, d_in
+  // 14336, d_out 4096: tiles of 32 rows without a split 31 us, 112 rows by four
+  // CTAs 20 us where that made one cluster more than fit at once.
+  long long best = -1;
+  for (int i = 0; i < 4; ++i) {
+    const int split = 1 << i, c = h->slots[i];
+    if (c <= 0 || (split > 1 && a.kb < 4 * split)) continue;
+    const int rows = std::min(128, std::max(8, cdiv(cdiv(a.n, c), 8) * 8)), tiles = cdiv(a.n, rows);
+    const long long cost =
+        (long long)cdiv(tiles, c) * cdiv(a.kb, split) * std::max(rows * 128 / 25, 200) + (split > 1 ? 3000 : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      a.split = split;
+      a.h = rows;
+    }
+  }
   CUtensorMap mW, mX;
   if (!code_map(&mW, h->desc.Wq, a.k, a.n, a.h) || !code_map(&mX, xq, a.k, a.T, a.each)) return SFFN_ERR_CUDA;
   return launched(launch_pdl(k_qlinear_cols<BN>, dim3(cdiv(a.n, a.h) * a.split), dim3(QL_THREADS), (size_t)QcCfg<BN>::SMEM,
@@ -368,6 +383,20 @@ extern "C" sffn_status sffn_qlinear_create(const sffn_qlinear_desc* desc, void* 
   e = e ? e : qlinear_rows_attr<1>();
   e = e ? e : qlinear_rows_attr<2>();
   e = e ? e : cudaStreamSynchronize(st);
+  h->slots[0] = n_sm;
+  for (int i = 1; i < 4 && !e; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1 << i;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(1 << i);
+    cfg.blockDim = dim3(QL_THREADS);
+    cfg.dynamicSmemBytes = QcCfg<16>::SMEM;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&h->slots[i], k_qlinear_cols<16>, &cfg);
+  }
   if (e || !get_encode()) {
     cudaGetLastError();
     free_on(dev, h->status);
@@ -401,6 +430,22 @@ extern "C" sffn_status sffn_qlinear_forward(sffn_qlinear_handle* h, const void* 
   if (T <= 128) return qlinear_cols<128>(h, xq, a, st);
   if (T <= 384) return qlinear_rows<1>(h, xq, a, st);
   return qlinear_rows<2>(h, xq, a, st);
+}
+
+extern "C" sffn_status sffn_qlinear_quantize_forward(sffn_qlinear_handle* h, const void* x, sffn_dtype x_dtype, int T,
+                                                     void* y, sffn_dtype y_dtype, void* workspace,
+                                                     size_t workspace_bytes, void* cuda_stream) {
+  if (!h || T < 0 || T > kMaxRows || !is_value_type(x_dtype) || !is_value_type(y_dtype)) return SFFN_ERR_INVALID_ARG;
+  if (T == 0) return SFFN_OK;
+  const size_t codes = ((size_t)T * h->desc.d_in + 15) & ~(size_t)15;
+  const size_t scales = (size_t)T * cdiv(h->desc.d_in, Q_GROUP) * sizeof(float);
+  if (!x || !y || !workspace || !aligned16(x) || !aligned16(y) || !aligned16(workspace) ||
+      workspace_bytes < codes + scales)
+    return SFFN_ERR_INVALID_ARG;
+  if (!on_device(h->dev)) return SFFN_ERR_INVALID_ARG;
+  float* xs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + codes);
+  const sffn_status s = sffn_quantize_rows(x, x_dtype, T, h->desc.d_in, workspace, xs, cuda_stream);
+  return s != SFFN_OK ? s : sffn_qlinear_forward(h, workspace, xs, T, y, y_dtype, cuda_stream);
 }
 
 extern "C" sffn_status sffn_qlinear_read_status(sffn_qlinear_handle* h, void* cuda_stream) {

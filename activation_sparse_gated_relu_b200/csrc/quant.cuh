@@ -15,6 +15,7 @@ __global__ void __launch_bounds__(256) k_quant_rows(const void* x, int T, int d,
   const long long n = (long long)T * gpr;
   const int l = threadIdx.x & 15;
   griddep_wait();
+  griddep_launch();   // the next kernel may set itself up meanwhile
   for (long long g0 = (long long)blockIdx.x * 16; g0 < n; g0 += (long long)gridDim.x * 16) {
     const long long g = g0 + (threadIdx.x >> 4);
     const long long t = g / gpr;

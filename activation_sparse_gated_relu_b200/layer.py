@@ -342,6 +342,7 @@ class Fp8Linear(_Handle):
         cp = _check(Ws, "Ws", (_FP32,), (_groups(n), _groups(k)), self.device)
         self.d_in, self.d_out, self.Wq, self.Ws = k, n, Wq, Ws
         self._create(sffn_qlinear_desc(d_in=k, d_out=n, Wq=wp, Ws=cp), stream)
+        self._call, self._call_values = self._lib.sffn_qlinear_forward, self._lib.sffn_qlinear_quantize_forward
 
     @classmethod
     def from_weight(cls, W, *, stream: Optional[int] = None) -> "Fp8Linear":
@@ -355,22 +356,26 @@ class Fp8Linear(_Handle):
         T, _ = _matrix(x, "x")
         dev, k = self.device, self.d_in
         dtype = _out_type(out)
-        codes = x.dtype is _FP8
-        xp = _check(x, "x", (_FP8,) if scale is not None else (_BF16, _FP32), (T, k), dev)
+        codes = scale is not None
+        xp = _check(x, "x", (_FP8,) if codes else _VALUES, (T, k), dev)
         if codes:
             cp = _check(scale, "scale", (_FP32,), (T, _groups(k)), dev)
         with _where(dev, stream):
-            if not codes:
-                q, scale = quantize_rows(x)
-                xp, cp = q.data_ptr(), scale.data_ptr()
             if y is None:
                 y = x.new_empty((T, self.d_out), dtype=dtype)
                 yp = y.data_ptr()
             else:
                 yp = _check(y, "y", (dtype,), (T, self.d_out), dev)
-                _apart(y, "y", x, scale, self.Wq, self.Ws)
-            _ok(self._lib.sffn_qlinear_forward(self.h, xp, cp, T, yp, _CODE[dtype], _raw_stream(dev)),
-                "Fp8Linear.forward")
+                _apart(y, "y", x, self.Wq, self.Ws, *((scale,) if codes else ()))
+            if codes:
+                s = self._call(self.h, xp, cp, T, yp, _CODE[dtype], _raw_stream(dev))
+            else:
+                n = (T * k + 15) // 16 * 16 + 4 * T * _groups(k)
+                work = x.new_empty(n, dtype=torch.uint8)
+                s = self._call_values(self.h, xp, _CODE[x.dtype], T, yp, _CODE[dtype], work.data_ptr(), n,
+                                      _raw_stream(dev))
+            if s:
+                raise SffnError(s, "Fp8Linear.forward")
         return y
 
     __call__ = forward

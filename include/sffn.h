@@ -561,6 +561,12 @@ sffn_status sffn_qlinear_create(const sffn_qlinear_desc* desc, void* cuda_stream
 /* y [T][d_out] bf16 or fp32, fully overwritten; T == 0 launches nothing. */
 sffn_status sffn_qlinear_forward(sffn_qlinear_handle* h, const void* xq, const float* xs, int T, void* y,
                                  sffn_dtype y_dtype, void* cuda_stream);
+/* The same from unquantised x [T][d_in] bf16 or fp32: sffn_quantize_rows into
+ * the workspace (device, 16-byte aligned: T·d_in bytes of codes rounded up to
+ * 16, then T·ceil(d_in/128) fp32 scales), then sffn_qlinear_forward. */
+sffn_status sffn_qlinear_quantize_forward(sffn_qlinear_handle* h, const void* x, sffn_dtype x_dtype, int T, void* y,
+                                          sffn_dtype y_dtype, void* workspace, size_t workspace_bytes,
+                                          void* cuda_stream);
 sffn_status sffn_qlinear_read_status(sffn_qlinear_handle* h, void* cuda_stream);   /* as sffn_read_status */
 sffn_status sffn_qlinear_destroy(sffn_qlinear_handle* h);
 

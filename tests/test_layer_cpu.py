@@ -115,6 +115,7 @@ def test_grouped_create_refuses(lib, kw, want):
 
 def test_calls_without_a_handle(lib):
     assert lib.sffn_qlinear_forward(None, P, P, 1, P, 0, None) == BAD
+    assert lib.sffn_qlinear_quantize_forward(None, P, 0, 1, P, 0, P, 1 << 20, None) == BAD
     assert lib.sffn_qlinear_read_status(None, None) == BAD
     assert lib.sffn_qlinear_destroy(None) == B.SFFN_OK
     assert lib.sffn_grouped_forward(None, P, P, 1, P, 0, None) == BAD
