@@ -20,6 +20,7 @@ using namespace sffn;
 namespace {
 
 constexpr int kMaxRows = 1 << 24;
+constexpr long long kMaxTiles = 1 << 30;   // tiles of a launch are counted in 32 bits
 
 sffn_status launched(cudaError_t e) { return e == cudaSuccess ? SFFN_OK : SFFN_ERR_CUDA; }
 
@@ -345,7 +346,7 @@ sffn_status qlinear_rows(const sffn_qlinear_handle* h, const void* xq, QlinArgs 
     }
   }
   const long long tiles = mt * cdiv(a.n, a.each);
-  if (tiles > 0x7FFFFFFFll) return SFFN_ERR_UNSUPPORTED;
+  if (tiles > kMaxTiles) return SFFN_ERR_UNSUPPORTED;
   CUtensorMap mX, mW, mY;
   if (!code_map(&mX, xq, a.k, a.T, 128) || !code_map(&mW, h->desc.Wq, a.k, a.n, a.each / CTAS) ||
       !out_map(&mY, a.y, a.y_f32, a.n, a.T))
@@ -505,9 +506,8 @@ sffn_status grouped_launch(const sffn_grouped_handle* h, const CUtensorMap& mA, 
 template <int MODE>
 sffn_status grouped_rows(const sffn_grouped_handle* h, const CUtensorMap& mA, const void* rows, const GroupedArgs& g,
                          cudaStream_t st) {
-  // tiles of 256 columns are at most R / 256 + E; their count is an int
   const long long tiles = (long long)cdiv(g.M, 128) * (g.R / 32 + g.E);
-  if (tiles > 0x7FFFFFFFll) return SFFN_ERR_UNSUPPORTED;
+  if (tiles > kMaxTiles) return SFFN_ERR_UNSUPPORTED;
   if (g.R >= 96ll * g.E) return grouped_launch<MODE, 2, 256>(h, mA, rows, g.K, g, tiles, st);
   if (g.R >= 24ll * g.E) return grouped_launch<MODE, 1, 128>(h, mA, rows, g.K, g, tiles, st);
   return grouped_launch<MODE, 1, 32>(h, mA, rows, g.K, g, tiles, st);
@@ -622,7 +622,7 @@ extern "C" sffn_status sffn_grouped_backward_weight(sffn_grouped_handle* h, cons
   CUtensorMap mx;
   if (!grouped_map(&mx, x, g.M, R, 0, 64)) return SFFN_ERR_CUDA;
   const long long tiles = (long long)g.E * cdiv(g.M, 256) * cdiv(g.N, 256);
-  if (tiles > 0x7FFFFFFFll) return SFFN_ERR_UNSUPPORTED;
+  if (tiles > kMaxTiles) return SFFN_ERR_UNSUPPORTED;
   return grouped_launch<GROUPED_DW, 2, 256>(h, mx, dy, g.N, g, tiles, st);
 }
 
