@@ -191,11 +191,28 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   __syncthreads();
   if (warp == 0) {   // first tile of each expert: a running sum over experts, 32 at a time
     const int mt = (args.M + 128 * CTAS - 1) / (128 * CTAS);
-    int base = 0;
+    int base = 0, end = 0;
     for (int e0 = 0; e0 < args.E; e0 += 32) {
       const int e = e0 + lane;
+      // A group starts no earlier than any before it ends: with offsets that run
+      // back and forth the rows, and so the tiles, would count many times.
+      const int b = e < args.E ? rb[e] : 0;
+      int last = b;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, last, o);
+        if (lane >= o) last = max(last, u);
+      }
+      last = max(last, end);
+      int before = __shfl_up_sync(0xFFFFFFFFu, last, 1);
+      if (lane == 0) before = end;
+      end = __shfl_sync(0xFFFFFFFFu, last, 31);
       int n = 0;
-      if (e < args.E) n = mt * (MODE == GROUPED_DW ? (args.N + BN - 1) / BN : (rb[e] - ra[e] + BN - 1) / BN);
+      if (e < args.E) {
+        ra[e] = max(ra[e], before);
+        rb[e] = max(b, ra[e]);
+        n = mt * (MODE == GROUPED_DW ? (args.N + BN - 1) / BN : (rb[e] - ra[e] + BN - 1) / BN);
+      }
       int s = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

@@ -580,9 +580,9 @@ sffn_status sffn_qlinear_destroy(sffn_qlinear_handle* h);
  * x [R][d_in], dy [R][d_out] bf16; sums fp32, rounded once.  Rows outside
  * every group are left as they were in y and dx; dW of an empty group is 0.
  * A row depends on no other row's values, not even NaN.  Offsets must not
- * decrease and lie in 0..R: the kernels clamp what does not and record
- * SFFN_ERR_DEVICE (sffn_grouped_read_status); the results of the groups
- * concerned are then undefined.
+ * decrease and lie in 0..R: the kernels clamp what does not (and start no group before all earlier
+ * ones end) and record SFFN_ERR_DEVICE (sffn_grouped_read_status); the results
+ * of the groups concerned are then undefined.
  * Limits: n_experts <= 1024, d_in % 8 == 0, d_out % 8 == 0, both <= 2^20. */
 #define SFFN_GROUPED_MAX_EXPERTS 1024
 typedef struct sffn_grouped_desc {

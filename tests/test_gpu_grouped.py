@@ -205,3 +205,15 @@ def test_gradients_against_differences():
         h = torch.zeros_like(W)
         h[i, o, c] = 0.5
         assert abs(loss(x, W + h) - loss(x, W - h) - dW[i, o, c]) < 1e-12
+
+
+def test_offsets_that_run_back_and_forth_count_no_row_twice():
+    # the first group has all rows, so the others, whatever they ask for, have none
+    op = GroupedLinear(ints(30, 64, 64, 64))
+    x, dy = ints(31, 40, 64), ints(32, 40, 64)
+    off = torch.tensor([0, 40] * 32 + [40], dtype=torch.int32, device="cuda")
+    y, g = op(x, off), op.backward(x, dy, off)
+    assert op.read_status() == SFFN_ERR_DEVICE
+    assert torch.equal(y, (x.float() @ op.W[0].float().t()).to(BF))
+    assert torch.equal(g["dx"], (dy.float() @ op.W[0].float()).to(BF))
+    assert torch.equal(g["dW"][0], dy.float().t() @ x.float()) and (g["dW"][1:] == 0).all()
