@@ -261,7 +261,8 @@ extern "C" sffn_status sffn_quantize_blocks(const void* W, sffn_dtype w_dtype, i
 struct sffn_qlinear_handle {
   sffn_qlinear_desc desc;
   int dev = 0, n_sm = 0;
-  int slots[4] = {0, 0, 0, 0};  // clusters of 1, 2, 4 and 8 CTAs that the GPU holds at once, one CTA per SM
+  // clusters of 1, 2, 4 and 8 CTAs that the GPU holds at once, one CTA per SM
+  int cols_slots[4] = {0, 0, 0, 0}, rows_slots[4] = {0, 0, 0, 0};
   uint32_t* status = nullptr;   // [4]
 };
 
@@ -300,21 +301,22 @@ cudaError_t qlinear_cols_attr() {
 
 template <int BN>
 sffn_status qlinear_cols(const sffn_qlinear_handle* h, const void* xq, QlinArgs a, cudaStream_t st) {
-  a.each = cdiv(a.T, 16) * 16;
   // How many CTAs share a tile's k, and how many weight rows a tile has: the
   // least time by a model of it, in cycles.  Every cluster that fits gets one
   // tile of even height, or several.  A block of k costs its bytes at 25 per
   // cycle and SM (the SMs' share of the memory bandwidth), and no less than its
-  // four MMAs, 200; a sum over a cluster costs 3000.  Measured at 13 tokens, d_in
-  // 14336, d_out 4096: tiles of 32 rows without a split 31 us, 112 rows by four
-  // CTAs 20 us where that made one cluster more than fit at once.
+  // MMAs and its pass through the epilogue; a sum over a cluster costs 3000.
+  // Measured with d_in 14336, d_out 4096: 13 tokens by 1, 2, 4, 8 CTAs 18.5, 14.6,
+  // 14.4, 24.6 us, 32 tokens 23.5, 17.0, 14.4, 27.1; d_in 4096, d_out 14336, 13
+  // tokens 12.8, 18.3, 25.8, 47.2.
+  constexpr int LEAST = BN <= 16 ? 220 : 300;
   long long best = -1;
   for (int i = 0; i < 4; ++i) {
-    const int split = 1 << i, c = h->slots[i];
+    const int split = 1 << i, c = h->cols_slots[i];
     if (c <= 0 || (split > 1 && a.kb < 4 * split)) continue;
     const int rows = std::min(128, std::max(8, cdiv(cdiv(a.n, c), 8) * 8)), tiles = cdiv(a.n, rows);
     const long long cost =
-        (long long)cdiv(tiles, c) * cdiv(a.kb, split) * std::max(rows * 128 / 25, 200) + (split > 1 ? 3000 : 0);
+        (long long)cdiv(tiles, c) * cdiv(a.kb, split) * std::max(rows * 128 / 25, LEAST) + (split > 1 ? 3000 : 0);
     if (best < 0 || cost < best) {
       best = cost;
       a.split = split;
@@ -322,37 +324,73 @@ sffn_status qlinear_cols(const sffn_qlinear_handle* h, const void* xq, QlinArgs 
     }
   }
   CUtensorMap mW, mX;
-  if (!code_map(&mW, h->desc.Wq, a.k, a.n, a.h) || !code_map(&mX, xq, a.k, a.T, a.each)) return SFFN_ERR_CUDA;
+  if (!code_map(&mW, h->desc.Wq, a.k, a.n, a.h) || !code_map(&mX, xq, a.k, a.T, cdiv(a.T, 16) * 16)) return SFFN_ERR_CUDA;
   return launched(launch_pdl(k_qlinear_cols<BN>, dim3(cdiv(a.n, a.h) * a.split), dim3(QL_THREADS), (size_t)QcCfg<BN>::SMEM,
                              st, a.split, mW, mX, a));
 }
 
-template <int CTAS>
+template <int BN>
 cudaError_t qlinear_rows_attr() {
-  return cudaFuncSetAttribute(k_qlinear_rows<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, QrCfg<CTAS>::SMEM);
+  return cudaFuncSetAttribute(k_qlinear_rows<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, QrCfg<BN>::SMEM);
 }
 
-template <int CTAS>
-sffn_status qlinear_rows(const sffn_qlinear_handle* h, const void* xq, QlinArgs a, cudaStream_t st) {
-  const long long mt = cdiv(a.T, 128 * CTAS), slots = h->n_sm / CTAS;
-  // columns per tile: what gives the least rounds x columns (a tile also costs
-  // about 32 columns' time whatever its width)
-  long long best = -1;
-  for (int n = 256; n >= 128; n -= 128) {
-    const long long cost = ((mt * cdiv(a.n, n) + slots - 1) / slots) * (n + 32);
-    if (best < 0 || cost < best) {
-      best = cost;
-      a.each = n;
-    }
-  }
-  const long long tiles = mt * cdiv(a.n, a.each);
-  if (tiles > kMaxTiles) return SFFN_ERR_UNSUPPORTED;
+template <int BN>
+sffn_status qlinear_rows_launch(const sffn_qlinear_handle* h, const void* xq, const QlinArgs& a, long long ctas,
+                                cudaStream_t st) {
   CUtensorMap mX, mW, mY;
-  if (!code_map(&mX, xq, a.k, a.T, 128) || !code_map(&mW, h->desc.Wq, a.k, a.n, a.each / CTAS) ||
+  if (!code_map(&mX, xq, a.k, a.T, 128) || !code_map(&mW, h->desc.Wq, a.k, a.n, BN) ||
       !out_map(&mY, a.y, a.y_f32, a.n, a.T))
     return SFFN_ERR_CUDA;
-  return launched(launch_pdl(k_qlinear_rows<CTAS>, dim3((unsigned)std::min(tiles, slots) * CTAS), dim3(QR_THREADS),
-                             (size_t)QrCfg<CTAS>::SMEM, st, CTAS, mX, mW, mY, a));
+  return launched(launch_pdl(k_qlinear_rows<BN>, dim3((unsigned)ctas), dim3(QR_THREADS), (size_t)QrCfg<BN>::SMEM, st,
+                             a.split, mX, mW, mY, a));
+}
+
+sffn_status qlinear_rows(const sffn_qlinear_handle* h, const void* xq, QlinArgs a, cudaStream_t st) {
+  // Tiles of 128 or 256 columns, and how many CTAs share a tile's k where all
+  // of the tiles fit at once: the least time by a model of it, in ns.  A block
+  // of k takes 360 with 128 columns and 565 with 256; a sum over a cluster costs
+  // 5000.  Measured in us, 128 and 256 columns: d_in 2048, d_out 8192, 256 tokens
+  // 9.8 and 13.3, 333 tokens (two rounds and one) 15.9 and 13.4, 4096 tokens 89 and
+  // 74; d_in 14336, d_out 4096, 768 tokens 81 and 60, 64 tokens by 1, 2, 4 CTAs
+  // 42, 26.7, 17.8; d_in 2048, d_out 8192, 128 tokens by 1 and 2 CTAs 9.3 and 11.3.
+  const long long mt = cdiv(a.T, 128), narrow = mt * cdiv(a.n, 128), wide = mt * cdiv(a.n, 256);
+  if (narrow > kMaxTiles) return SFFN_ERR_UNSUPPORTED;
+  a.split = 1;
+  const long long cost_wide = cdiv(wide, h->n_sm) * (a.kb * 565ll + 1500);
+  long long best = cdiv(narrow, h->n_sm) * (a.kb * 360ll + 400);
+  for (int i = 1; i < 4; ++i) {
+    const int split = 1 << i;
+    if (narrow > h->rows_slots[i] || a.kb < 4 * split) continue;
+    const long long cost = cdiv(a.kb, split) * 360ll + 5000;
+    if (cost < best) {
+      best = cost;
+      a.split = split;
+    }
+  }
+  if (cost_wide >= best)
+    return qlinear_rows_launch<128>(h, xq, a, a.split > 1 ? narrow * a.split : std::min<long long>(narrow, h->n_sm), st);
+  a.split = 1;
+  return qlinear_rows_launch<256>(h, xq, a, std::min<long long>(wide, h->n_sm), st);
+}
+
+// Clusters of 2, 4 and 8 CTAs of a kernel that the GPU holds at once.
+template <typename Kernel>
+cudaError_t count_clusters(Kernel kernel, int threads, int smem, int (&slots)[4]) {
+  cudaError_t e = cudaSuccess;
+  for (int i = 1; i < 4 && !e; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1 << i;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(1 << i);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&slots[i], kernel, &cfg);
+  }
+  return e;
 }
 
 }  // namespace
@@ -379,25 +417,12 @@ extern "C" sffn_status sffn_qlinear_create(const sffn_qlinear_desc* desc, void* 
   cudaError_t e = cudaMemsetAsync(h->status, 0, 16, st);
   e = e ? e : qlinear_cols_attr<16>();
   e = e ? e : qlinear_cols_attr<32>();
-  e = e ? e : qlinear_cols_attr<64>();
-  e = e ? e : qlinear_cols_attr<128>();
-  e = e ? e : qlinear_rows_attr<1>();
-  e = e ? e : qlinear_rows_attr<2>();
+  e = e ? e : qlinear_rows_attr<128>();
+  e = e ? e : qlinear_rows_attr<256>();
   e = e ? e : cudaStreamSynchronize(st);
-  h->slots[0] = n_sm;
-  for (int i = 1; i < 4 && !e; ++i) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1 << i;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(1 << i);
-    cfg.blockDim = dim3(QL_THREADS);
-    cfg.dynamicSmemBytes = QcCfg<16>::SMEM;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&h->slots[i], k_qlinear_cols<16>, &cfg);
-  }
+  h->cols_slots[0] = h->rows_slots[0] = n_sm;
+  e = e ? e : count_clusters(k_qlinear_cols<16>, QL_THREADS, QcCfg<16>::SMEM, h->cols_slots);
+  e = e ? e : count_clusters(k_qlinear_rows<128>, QR_THREADS, QrCfg<128>::SMEM, h->rows_slots);
   if (e || !get_encode()) {
     cudaGetLastError();
     free_on(dev, h->status);
@@ -425,12 +450,13 @@ extern "C" sffn_status sffn_qlinear_forward(sffn_qlinear_handle* h, const void* 
   a.y_f32 = y_dtype == SFFN_FP32;
   a.status = h->status;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  // Up to 32 tokens cost less as the MMA's columns than as a quarter of its rows:
+  // measured at 16 / 32 / 40 tokens, d_in 4096, d_out 14336, 16 columns 12.8, 32
+  // columns 13.9 / 14.3, 64 columns 15.4 / 16.1 / 16.4 (taken out), rows 15.9 us at
+  // all three; d_in 2048, d_out 8192: 5.7, 6.7 / 7.2, 9.8 / 10.2 / 10.3, rows 9.8.
   if (T <= 16) return qlinear_cols<16>(h, xq, a, st);
   if (T <= 32) return qlinear_cols<32>(h, xq, a, st);
-  if (T <= 64) return qlinear_cols<64>(h, xq, a, st);
-  if (T <= 128) return qlinear_cols<128>(h, xq, a, st);
-  if (T <= 384) return qlinear_rows<1>(h, xq, a, st);
-  return qlinear_rows<2>(h, xq, a, st);
+  return qlinear_rows(h, xq, a, st);
 }
 
 extern "C" sffn_status sffn_qlinear_quantize_forward(sffn_qlinear_handle* h, const void* x, sffn_dtype x_dtype, int T,
@@ -508,8 +534,18 @@ sffn_status grouped_rows(const sffn_grouped_handle* h, const CUtensorMap& mA, co
                          cudaStream_t st) {
   const long long tiles = (long long)cdiv(g.M, 128) * (g.R / 32 + g.E);
   if (tiles > kMaxTiles) return SFFN_ERR_UNSUPPORTED;
-  if (g.R >= 96ll * g.E) return grouped_launch<MODE, 2, 256>(h, mA, rows, g.K, g, tiles, st);
-  if (g.R >= 24ll * g.E) return grouped_launch<MODE, 1, 128>(h, mA, rows, g.K, g, tiles, st);
+  // Columns per tile, by the mean rows of an expert, since a second tile of
+  // columns reads the expert's weight again.  Measured in us with 32, 128, 256
+  // columns (256: CTA pairs), 8 experts of 4096 x 14336 | 32 of 2048 x 1024:
+  //   mean rows    forward                               input gradient
+  //       2        129 138 141  |  25.0 25.6 26.5        137 133 136  |  21.2 20.8 22.3
+  //      16        154 164 167  |  25.3 25.7 27.2        149 141 148  |  25.7 25.6 27.2
+  //      32                     |  29.2 27.1 28.7                     |  30.5 26.4 28.5
+  //     104        391 171 179  |  61.4 28.7 30.8        396 152 153  |  65.0 28.6 30.9
+  //     120        419 192 178  |  68.4 35.9 31.2        446 193 159  |  68.7 32.6 31.4
+  //     256                     |   126 49.7 43.1                     |   133 47.9 43.2
+  if (g.R >= 112ll * g.E) return grouped_launch<MODE, 2, 256>(h, mA, rows, g.K, g, tiles, st);
+  if (g.R >= (MODE == GROUPED_FWD ? 24ll : 8ll) * g.E) return grouped_launch<MODE, 1, 128>(h, mA, rows, g.K, g, tiles, st);
   return grouped_launch<MODE, 1, 32>(h, mA, rows, g.K, g, tiles, st);
 }
 

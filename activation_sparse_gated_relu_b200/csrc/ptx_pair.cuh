@@ -34,19 +34,6 @@ __device__ __forceinline__ void mbar_release_cluster(uint32_t addr) {
 __device__ __forceinline__ void mbar_expect_cluster(uint32_t addr, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(bytes) : "memory");
 }
-// Whether the phase has completed, without waiting (try_wait may suspend the
-// thread for a while).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // True in one lane of a converged warp.  Copies and MMAs take their operands
 // from uniform registers; behind this predicate (rather than a lane number)
 // the compiler knows that a single lane is active and needs no loop over lanes.

@@ -4,20 +4,27 @@
 //   y[t][n] = sum_b xs[t][b] · Ws[n/128][b] · sum_{k in b} xq[t][k] · Wq[n][k]
 //
 // The tensor core adds up one block (four MMAs of 32) in TMEM; each block's
-// sums are then scaled and added in fp32 registers, while the MMAs of the next
-// blocks run in other TMEM columns.
+// sums are then scaled and added in fp32 registers, two columns at a time,
+// while the MMAs of the next blocks run in other TMEM columns.
 //
-// k_qlinear_cols: few tokens.  Weight rows are the MMA's 128 rows (TMEM
+// k_qlinear_cols: up to 32 tokens.  Weight rows are the MMA's 128 rows (TMEM
 // lanes), tokens its columns, so that a token costs little and W is read
-// once.  Bound by W's bytes.  An MMA of 128 x 16 x 32 takes 45 cycles however
-// many of its rows are used, and looking at a barrier 50 to 100, so a stage is
-// several blocks with one barrier each way, and a narrow weight (few rows,
+// once.  Bound by W's bytes: one token, d_in 4096, d_out 14336, 59 MB, 12.6 us of
+// which some 4 are launch and set-up.  An MMA of 128 x 16 x 32 takes 45 cycles
+// however many of its rows are used, and looking at a barrier 50 to 100, so a
+// stage is two blocks with one barrier each way, and a narrow weight (few rows,
 // long k) is cut along k over the CTAs of a cluster, which add their sums up
-// through distributed shared memory in a fixed order.
+// through distributed shared memory in a fixed order: 13 tokens, d_in 14336,
+// d_out 4096, 18.5 us without and 14.4 with.
 //
-// k_qlinear_rows: many tokens.  Tokens are the MMA's rows, so that a token's
-// scale is one register per thread; CTA pairs share a tile of 256 tokens.
-// Bound by the tensor cores.
+// k_qlinear_rows: more tokens.  Tokens are the MMA's rows, so that a token's
+// scale is one register per thread.  4096 tokens, d_in 4096, d_out 14336: 252 us,
+// 1.9 PFLOP/s.  A block of 128 x 256 takes about 1000 cycles: 512 are MMAs, 768
+// the least that shared memory needs at 128 bytes a cycle (48 KB in by copies, 48
+// KB out to the MMAs), and the sums' way from TMEM takes 560.  CTA pairs, which
+// halve the weights' part, took 259 us (the second CTA's epilogue has to signal
+// the first); halves of 128 columns with barriers of their own 277 (the tokens
+// are read from shared memory twice).
 #pragma once
 
 #include "ptx_pair.cuh"
@@ -41,8 +48,7 @@ struct QlinArgs {
   void* y;              // [T][n], bf16 or fp32
   int T, n, k, kb;
   int h;                // k_qlinear_cols: weight rows per CTA
-  int each;             // tokens per CTA (k_qlinear_cols, a multiple of 16), columns per tile (k_qlinear_rows)
-  int split;            // k_qlinear_cols: CTAs of a cluster, each with a part of k
+  int split;            // CTAs of a cluster, each with a part of k
   int y_f32;
   uint32_t* status;
 };
@@ -52,26 +58,43 @@ __device__ __forceinline__ void put_y(void* y, int f32, size_t at, float v) {
   else reinterpret_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16(v);
 }
 
+// v[q] = the sum over the cluster's CTAs, in order, of their shared memory's
+// float at addr + q · step.  All loads go out before the first sum.
+template <int N>
+__device__ __forceinline__ void cluster_sums(uint32_t addr, uint32_t step, int split, float (&v)[N]) {
+  float u[8][N];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (r < split) {
+      const uint32_t from = cluster_addr(addr, (uint32_t)r);
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u[r][q]) : "r"(from + (uint32_t)q * step) : "memory");
+    }
+#pragma unroll
+  for (int q = 0; q < N; ++q) v[q] = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (r < split)
+#pragma unroll
+      for (int q = 0; q < N; ++q) v[q] += u[r][q];
+}
+
 template <int BN>
 struct QcCfg {
-  static constexpr int KS = BN <= 64 ? 2 : 1;            // 128-wide blocks per stage
+  static constexpr int KS = 2;                           // 128-wide blocks per stage
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = KS * (A_BYTES + B_BYTES);
   static constexpr int SLOT = BN + 4;                    // scales of a block: tokens, two weight blocks
   static constexpr int SCALES = KS * SLOT * 4;
   static constexpr int FIXED = 1024 + 512;
-  // An even number: the MMA threads and (up to 64 columns) the epilogue
-  // warpgroups take every other stage, and each may only ever wait on barriers
-  // whose every phase it waits for: a phase's parity says nothing about the
-  // phases it has not seen.
+  // An even number: the MMA threads and the epilogue warpgroups take every
+  // other stage, and each may only ever wait on barriers whose every phase it
+  // waits for: a phase's parity says nothing about the phases it has not seen.
   static constexpr int RAW = (QL_SMEM - FIXED) / (STAGE + SCALES);
   static constexpr int STAGES = (RAW > 8 ? 8 : RAW) & ~1;
   static constexpr int SMEM = FIXED + STAGES * (STAGE + SCALES);
   static constexpr int NBUF = 4;                         // TMEM accumulators, KS · BN columns each
-  // Up to 64 columns the two epilogue warpgroups take every other stage, above
-  // that they halve the columns.
-  static constexpr bool ALT = BN <= 64;
-  static constexpr int COLS = ALT ? BN : BN / 2;         // columns per epilogue thread
 };
 
 template <int BN>
@@ -97,8 +120,7 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = a.split > 1 ? (int)cluster_rank() : 0;
-  const int m0 = (blockIdx.x / a.split) * a.h, n0 = blockIdx.y * a.each;
-  const int cols = min(a.each, a.T - n0), bn = (cols + 15) & ~15;
+  const int m0 = (blockIdx.x / a.split) * a.h, cols = a.T, bn = (cols + 15) & ~15;
   // this CTA's blocks of k
   const int kb0 = (int)((long long)a.kb * rank / a.split), kb1 = (int)((long long)a.kb * (rank + 1) / a.split);
   const int ns = (kb1 - kb0 + KS - 1) / KS;
@@ -108,11 +130,11 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&sfull[s], 32);
-      mbar_init(&sempty[s], Cfg::ALT ? 4 : QL_EPI_WARPS);
+      mbar_init(&sempty[s], QL_EPI_WARPS / 2);
     }
     for (int b = 0; b < NBUF; ++b) {
       mbar_init(&accfull[b], 1);
-      mbar_init(&accfree[b], Cfg::ALT ? 4 : QL_EPI_WARPS);
+      mbar_init(&accfree[b], QL_EPI_WARPS / 2);
     }
     mbar_init(mma_done, 2);
     *abort_flag = 0;
@@ -145,10 +167,10 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
         uint8_t* st = smem + (size_t)s * Cfg::STAGE;
         const int kb = kb0 + i * KS, nb = min(KS, kb1 - kb);
         const uint32_t bar = smem_u32(&full[s]);
-        mbar_expect_tx(&full[s], (uint32_t)(nb * (a.h + a.each) * 128));
+        mbar_expect_tx(&full[s], (uint32_t)(nb * (a.h + bn) * 128));
         for (int j = 0; j < nb; ++j) {
           tma_2d<1>(st + j * Cfg::A_BYTES, &mW, bar, (kb + j) * 128, m0);
-          tma_2d<1>(st + KS * Cfg::A_BYTES + j * Cfg::B_BYTES, &mX, bar, (kb + j) * 128, n0);
+          tma_2d<1>(st + KS * Cfg::A_BYTES + j * Cfg::B_BYTES, &mX, bar, (kb + j) * 128, 0);
         }
       }
       __syncwarp();
@@ -175,7 +197,7 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
         float* slot = slots + (s * KS + j) * Cfg::SLOT;
 #pragma unroll
         for (int col = lane; col < BN; col += 32)
-          copy4_async(slot + col, a.xs + (size_t)(n0 + min(col, cols - 1)) * a.kb + kb, col < cols);
+          copy4_async(slot + col, a.xs + (size_t)min(col, cols - 1) * a.kb + kb, col < cols);
         if (lane < 2) copy4_async(slot + BN + lane, ws + kb, true);
       }
       copies_arrive(&sfull[s]);
@@ -227,16 +249,15 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     }
   } else {
     // ------------------------------------------------------------- epilogue
-    constexpr int COLS = Cfg::COLS;
+    // Two warpgroups, every other stage each.
     const int wg = warp >> 2, row = (warp & 3) * 32 + lane, m = m0 + row;
-    const int c0 = Cfg::ALT ? 0 : wg * COLS;            // first column of this thread
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const bool in = row < a.h && m < a.n;
     const int blk = in ? m / Q_GROUP - m0 / Q_GROUP : 0;   // h <= 128: one of two weight blocks
-    float acc[COLS];
+    uint64_t sum[BN / 2];   // of two columns each
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
-    for (int i = Cfg::ALT ? wg : 0; i < ns; i += Cfg::ALT ? 2 : 1) {
+    for (int i = 0; i < BN / 2; ++i) sum[i] = 0;
+    for (int i = wg; i < ns; i += 2) {
       const int s = i % STAGES, b = i % NBUF, kb = kb0 + i * KS;
       // A failed wait is not acted on (nothing is stored then): leaving the
       // loop from its middle would cost a select per sum.
@@ -247,19 +268,17 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       for (int j = 0; j < KS; ++j) {
         if (kb + j < kb1) {
           const float* slot = slots + (s * KS + j) * Cfg::SLOT;
-          const float4* xs = reinterpret_cast<const float4*>(slot + c0);
-          const float w = slot[BN + blk];
+          const float4* xs = reinterpret_cast<const float4*>(slot);
+          const uint64_t w = pack2(slot[BN + blk], slot[BN + blk]);
 #pragma unroll
-          for (int c = 0; c < COLS; c += 16) {
-            float v[16];
-            tmem_get16(tlane + (uint32_t)((b * KS + j) * BN + c0 + c), v);
+          for (int c = 0; c < BN; c += 16) {
+            uint64_t v[8];
+            tmem_get16x2(tlane + (uint32_t)((b * KS + j) * BN + c), v);
 #pragma unroll
-            for (int u = 0; u < 16; u += 4) {
-              const float4 x = xs[(c + u) / 4];
-              acc[c + u] = fmaf(v[u], x.x * w, acc[c + u]);
-              acc[c + u + 1] = fmaf(v[u + 1], x.y * w, acc[c + u + 1]);
-              acc[c + u + 2] = fmaf(v[u + 2], x.z * w, acc[c + u + 2]);
-              acc[c + u + 3] = fmaf(v[u + 3], x.w * w, acc[c + u + 3]);
+            for (int u = 0; u < 8; u += 2) {
+              const float4 x = xs[c / 4 + u / 2];
+              sum[c / 2 + u] = fma2(v[u], mul2(pack2(x.x, x.y), w), sum[c / 2 + u]);
+              sum[c / 2 + u + 1] = fma2(v[u + 1], mul2(pack2(x.z, x.w), w), sum[c / 2 + u + 1]);
             }
           }
         }
@@ -271,29 +290,28 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
         mbar_arrive(&sempty[s]);
       }
     }
+    float acc[BN];
+#pragma unroll
+    for (int i = 0; i < BN / 2; ++i) unpack2(sum[i], acc[2 * i], acc[2 * i + 1]);
     float* ex = reinterpret_cast<float*>(smem);       // [BN][128], in the ring's memory (see below)
-    if (Cfg::ALT || a.split > 1) {
-      // Once both warpgroups have seen their last stage, every copy and MMA of
-      // this CTA has completed and the ring is free.
-      named_bar_sync(1, QL_EPI_WARPS * 32);
-      if (wg == 1)
+    // Once both warpgroups have seen their last stage, every copy and MMA of
+    // this CTA has completed and the ring is free.
+    named_bar_sync(1, QL_EPI_WARPS * 32);
+    if (wg == 1)
 #pragma unroll
-        for (int i = 0; i < COLS; ++i) ex[(c0 + i) * 128 + row] = acc[i];
-    }
-    if (Cfg::ALT) {   // the odd stages' sums join the even stages'
-      named_bar_sync(1, QL_EPI_WARPS * 32);
-      if (wg == 0)
+      for (int i = 0; i < BN; ++i) ex[i * 128 + row] = acc[i];
+    named_bar_sync(1, QL_EPI_WARPS * 32);
+    if (wg == 0) {   // the odd stages' sums join the even stages'
 #pragma unroll
-        for (int i = 0; i < COLS; ++i) acc[i] += ex[i * 128 + row];
-    }
-    if (a.split > 1) {
-      if (wg == 0)
+      for (int i = 0; i < BN; ++i) acc[i] += ex[i * 128 + row];
+      if (a.split > 1) {
 #pragma unroll
-        for (int i = 0; i < COLS; ++i) ex[(c0 + i) * 128 + row] = acc[i];
-    } else if (in && !*abort_flag && !(Cfg::ALT && wg == 1)) {
+        for (int i = 0; i < BN; ++i) ex[i * 128 + row] = acc[i];
+      } else if (in && !*abort_flag) {
 #pragma unroll
-      for (int i = 0; i < COLS; ++i)
-        if (c0 + i < cols) put_y(a.y, a.y_f32, (size_t)(n0 + c0 + i) * a.n + m, acc[i]);
+        for (int i = 0; i < BN; ++i)
+          if (i < cols) put_y(a.y, a.y_f32, (size_t)i * a.n + m, acc[i]);
+      }
     }
   }
   __syncwarp();
@@ -304,17 +322,13 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     const int row = threadIdx.x & 127, m = m0 + row;
     if (threadIdx.x < QL_EPI_WARPS * 32 && row < a.h && m < a.n && !*abort_flag) {
       const uint32_t ex = smem_u32(smem);
-      for (int c = rank + a.split * (threadIdx.x >> 7); c < cols; c += 2 * a.split) {
-        float v = 0.0f;
-        for (int r = 0; r < a.split; ++r) {
-          float u;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                       : "=f"(u)
-                       : "r"(cluster_addr(ex + (uint32_t)(c * 128 + row) * 4, (uint32_t)r))
-                       : "memory");
-          v += u;
-        }
-        put_y(a.y, a.y_f32, (size_t)(n0 + c) * a.n + m, v);
+      const int step = 2 * a.split;
+      for (int c = rank + a.split * (threadIdx.x >> 7); c < cols; c += 4 * step) {   // up to cols + 3 steps < BN + 64
+        float v[4];
+        cluster_sums<4>(ex + (uint32_t)(c * 128 + row) * 4, (uint32_t)step * 512, a.split, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c + step * q < cols) put_y(a.y, a.y_f32, (size_t)(c + step * q) * a.n + m, v[q]);
       }
     }
     __syncwarp();
@@ -328,13 +342,14 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
 }
 
 // ---------------------------------------------------------------- many tokens
-// Every block's sums (128 x 256 per CTA) pass from TMEM through registers, in
-// the time of the next block's four MMAs (512 cycles): 128 columns per thread,
-// 128 of its registers their sums (384 threads leave 168 each), multiplied and
-// added two at a time, since single multiply-adds alone would take the 512.
-constexpr int QR_EPI_WARPS = 8;
-constexpr int QR_PRODUCER = QR_EPI_WARPS, QR_SCALE = QR_EPI_WARPS + 1, QR_MMA = QR_EPI_WARPS + 2;   // + 3 idles
-constexpr int QR_THREADS = (QR_EPI_WARPS + 4) * 32;
+// Every block's sums (128 x BN per CTA) pass from TMEM through registers, while
+// the next block's MMAs (four of 128 cycles at 256 columns) run.  A warp spends
+// most of that in latencies (a barrier, its scales, its reads of TMEM), so
+// sixteen warps share it, a quarter of the columns each: a block of 128 columns
+// took 540 ns with eight warps that read 256 whatever the tile, 360 so.
+constexpr int QR_EPI_WARPS = 16;
+constexpr int QR_PRODUCER = QR_EPI_WARPS, QR_SCALE = QR_EPI_WARPS + 1, QR_MMA = QR_EPI_WARPS + 2;
+constexpr int QR_THREADS = (QR_EPI_WARPS + 3) * 32;
 // Scales of four blocks: 128 tokens' and 2 weight blocks', four values
 // each.  Every token's come from another line, with the latency of L2: 16
 // blocks of them are in flight.  The MMAs' operands and the copies that bring
@@ -345,14 +360,17 @@ constexpr int QR_SLOTS = 4, QR_SLOT = 4 * 130;
 // tiled copies: a thread's own stores (16 bytes of 32 rows each) took as long
 // as ten blocks of MMAs.
 constexpr int QR_OUT = 32 * 64;
-template <int CTAS>
+// BN: weight rows per tile, 128 or 256.
+template <int BN>
 struct QrCfg {
-  static constexpr int BN = 256;                        // weight rows per tile, at most
-  static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / CTAS * 128;
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int FIXED = 1024 + 512 + QR_SLOTS * QR_SLOT * 4 + QR_EPI_WARPS * QR_OUT;
-  static constexpr int STAGES = (QL_SMEM - FIXED) / STAGE;
+  static constexpr int RAW = (QL_SMEM - FIXED) / STAGE;
+  static constexpr int STAGES = RAW > 6 ? 6 : RAW;
   static constexpr int SMEM = FIXED + STAGES * STAGE;
+  static constexpr int NBUF = 512 / BN;                 // TMEM accumulators
+  static constexpr int COLS = BN / 4;                   // columns per epilogue thread
 };
 
 // A warp's 32 rows of 64 bytes leave; rows and columns past the end are not written.
@@ -366,42 +384,45 @@ __device__ __forceinline__ void store_rows(const CUtensorMap* map, const uint8_t
   __syncwarp();
 }
 
-// Tile w: 128 · CTAS tokens (fastest) and `each` weight rows (128 or 256, so
-// that half of them lie in one weight block).
-template <int CTAS>
+// Tile w: 128 tokens (fastest) and BN weight rows, each by the CTAs of a cluster
+// that share k (split > 1: one tile per cluster).
+template <int BN>
 __global__ void __launch_bounds__(QR_THREADS, 1)
 k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW,
                const __grid_constant__ CUtensorMap mY, const QlinArgs a) {
-  using Cfg = QrCfg<CTAS>;
-  constexpr int STAGES = Cfg::STAGES, BN = Cfg::BN;
+  using Cfg = QrCfg<BN>;
+  constexpr int STAGES = Cfg::STAGES, NBUF = Cfg::NBUF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stage_out = smem + STAGES * Cfg::STAGE;                       // [QR_EPI_WARPS][QR_OUT]
   float* slots = reinterpret_cast<float*>(stage_out + QR_EPI_WARPS * QR_OUT);   // [QR_SLOTS][QR_SLOT]
   uint64_t* full = reinterpret_cast<uint64_t*>(slots + QR_SLOTS * QR_SLOT);
   uint64_t* empty = full + STAGES;
-  uint64_t* accfull = empty + STAGES;   // [2]
-  uint64_t* accfree = accfull + 2;      // [2]; the second CTA's epilogue signals its own, see the relay
-  uint64_t* sfull = accfree + 2;        // [QR_SLOTS] scales
+  uint64_t* accfull = empty + STAGES;   // [NBUF]
+  uint64_t* accfree = accfull + NBUF;   // [NBUF]
+  uint64_t* sfull = accfree + NBUF;     // [QR_SLOTS] scales
   uint64_t* sfree = sfull + QR_SLOTS;
   uint64_t* mma_done = sfree + QR_SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((2 * STAGES + 5 + 2 * QR_SLOTS) * 8 + 8 <= 512, "barrier area");
+  static_assert((2 * STAGES + 2 * NBUF + 1 + 2 * QR_SLOTS) * 8 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
-  const int mt = (a.T + 128 * CTAS - 1) / (128 * CTAS), n_tiles = mt * ((a.n + a.each - 1) / a.each);
-  const int KB = a.kb, half = a.each / CTAS, walk0 = blockIdx.x / CTAS, n_walk = gridDim.x / CTAS;
+  const int mt = (a.T + 127) / 128, n_tiles = mt * ((a.n + BN - 1) / BN);
+  const int walk0 = blockIdx.x / a.split, n_walk = gridDim.x / a.split;
+  const int rank = a.split > 1 ? (int)cluster_rank() : 0;
+  // this CTA's blocks of k
+  const int kb0 = (int)((long long)a.kb * rank / a.split);
+  const int KB = (int)((long long)a.kb * (rank + 1) / a.split) - kb0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], CTAS);
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NBUF; ++b) {
       mbar_init(&accfull[b], 1);
-      mbar_init(&accfree[b], QR_EPI_WARPS + (CTAS == 2 && rank == 0 ? 1 : 0));
+      mbar_init(&accfree[b], QR_EPI_WARPS);
     }
     for (int j = 0; j < QR_SLOTS; ++j) {
       mbar_init(&sfull[j], 32);
@@ -411,14 +432,15 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == QR_MMA) pair_tmem_alloc<CTAS>(tmem_slot, 512);
+  if (warp == QR_MMA) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
   if (warp == QR_PRODUCER && lane == 0) {
     tma_prefetch_desc(&mX);
     tma_prefetch_desc(&mW);
   }
-  __syncwarp();
   tc_fence_before();
-  if (CTAS == 2) cluster_sync();   // the barriers of both CTAs are ready
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -431,18 +453,16 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
       int s = 0;
       uint32_t ph = 1;
       for (int w = walk0; w < n_tiles && ok; w += n_walk) {
-        const int m0 = (w % mt * CTAS + (int)rank) * 128, n0 = w / mt * a.each + (int)rank * half;
+        const int m0 = w % mt * 128, n0 = w / mt * BN;
         for (int kb = 0; kb < KB; ++kb) {
           ok = mbar_wait_warp(&empty[s], ph, abort_flag, a.status);   // the first round passes
           if (!ok) break;
           if (elect_one()) {
             uint8_t* st = smem + (size_t)s * Cfg::STAGE;
-            const uint32_t bytes = (uint32_t)(128 + half) * 128;
-            const uint32_t bar = CTAS == 2 ? cluster_addr(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-            if (CTAS == 2) mbar_expect_cluster(bar, bytes);
-            else mbar_expect_tx(&full[s], bytes);
-            tma_2d<CTAS>(st, &mX, bar, kb * 128, m0);
-            tma_2d<CTAS>(st + Cfg::A_BYTES, &mW, bar, kb * 128, n0);
+            const uint32_t bar = smem_u32(&full[s]);
+            mbar_expect_tx(&full[s], Cfg::STAGE);
+            tma_2d<1>(st, &mX, bar, (kb0 + kb) * 128, m0);
+            tma_2d<1>(st + Cfg::A_BYTES, &mW, bar, (kb0 + kb) * 128, n0);
           }
           __syncwarp();
           if (++s == STAGES) {
@@ -462,11 +482,11 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
       uint32_t jph = 1;
       bool ok = true;
       for (int w = walk0; w < n_tiles && ok; w += n_walk) {
-        const int m0 = (w % mt * CTAS + (int)rank) * 128, nb0 = w / mt * a.each / Q_GROUP;
+        const int m0 = w % mt * 128, nb0 = w / mt * (BN / Q_GROUP);
         const float* x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = a.xs + (size_t)min(m0 + i * 32 + lane, a.T - 1) * KB;
-        const float* ws = a.Ws + (size_t)min(nb0 + (lane & 1), nblk - 1) * KB;
+        for (int i = 0; i < 4; ++i) x[i] = a.xs + (size_t)min(m0 + i * 32 + lane, a.T - 1) * a.kb + kb0;
+        const float* ws = a.Ws + (size_t)min(nb0 + (lane & 1), nblk - 1) * a.kb + kb0;
         for (int kb = 0; kb < KB; kb += 4) {
           ok = mbar_wait_warp(&sfree[j], jph, abort_flag, a.status);   // the first round passes
           if (!ok) break;
@@ -486,11 +506,10 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
         }
       }
       copies_wait_all();
-    } else if (warp == QR_MMA && rank == 0) {
+    } else {
       // --------------------------------------------------------- MMA issuer
-      // One thread (of the pair's first CTA).
       if (elect_one()) {
-        const uint32_t idesc = idesc_e4m3_f32(128 * CTAS, a.each);
+        const uint32_t idesc = idesc_e4m3_f32(128, BN);
         const uint64_t desc0 = sdesc_k_sw128(smem_u32(smem));
         bool ok = true;
         int s = 0, b = 0;
@@ -501,12 +520,12 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
             if (!ok) break;
             tc_fence_after();
             const uint64_t ad = desc0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = ad + Cfg::A_BYTES / 16;
-            const uint32_t d = tmem + (uint32_t)(b * BN);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pair_mma<CTAS, true>(d, ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-            pair_commit<CTAS>(&accfull[b]);
-            pair_commit<CTAS>(&empty[s]);
-            b ^= 1;
+            for (int k = 0; k < 4; ++k)
+              pair_mma<1, true>(tmem + (uint32_t)(b * BN), ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+            tc_commit(&accfull[b]);
+            tc_commit(&empty[s]);
+            b = (b + 1) & (NBUF - 1);
             if (!b) bph ^= 1;
             if (++s == STAGES) {
               s = 0;
@@ -514,38 +533,21 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
             }
           }
         }
-        pair_commit<CTAS>(mma_done);
+        tc_commit(mma_done);
       }
-    } else if (CTAS == 2 && warp == QR_MMA) {
-      // -------------------------------------------------------------- relay
-      // A signal to the other CTA takes a warp some 300 cycles: the second
-      // CTA's epilogue signals here, and this warp passes one signal on.
-      const uint32_t free0 = cluster_addr(smem_u32(&accfree[0]), 0);
-      int b = 0;
-      uint32_t bph = 0;
-      bool ok = true;
-      for (int w = walk0; w < n_tiles && ok; w += n_walk)
-        for (int kb = 0; kb < KB; ++kb) {
-          ok = mbar_wait_warp(&accfree[b], bph, abort_flag, a.status);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_cluster(free0 + 8 * b);
-          b ^= 1;
-          if (!b) bph ^= 1;
-        }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------- epilogue
-    // A thread has one token and half of the tile's columns, at most 128.
-    // Tiles narrower than 256 are read as if they were not: what the unused
-    // columns hold is never stored, and a test would cost a select per sum.
-    const int wg = warp >> 2, hc = a.each / 2, row = (warp & 3) * 32 + lane;
-    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(wg * hc);
+    // A thread has one token and a quarter of the tile's columns.
+    constexpr int COLS = Cfg::COLS;
+    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(quarter * COLS);
+    const int blk = quarter * COLS / Q_GROUP;   // these columns' weight block, counted from the tile's first
     int b = 0, j = 0;
     uint32_t bph = 0, jph = 0;
     float sc[4];
-    const int blk = wg * hc / Q_GROUP;   // this half's weight block, counted from the tile's first
-    // the next four blocks' scales
+        // the next four blocks' scales
     auto scales = [&]() -> bool {
       if (!mbar_wait_warp(&sfull[j], jph, abort_flag, a.status)) return false;
       const float4* slot = reinterpret_cast<const float4*>(slots + j * QR_SLOT);
@@ -562,72 +564,75 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     // Left at once when a wait fails: going on to the end of a loop from the
     // middle would keep both sides' sums alive.
     auto run = [&]() {
-    if (walk0 < n_tiles && !scales()) return;
-    for (int w = walk0; w < n_tiles; w += n_walk) {
-      const int t = (w % mt * CTAS + (int)rank) * 128 + row, n0 = w / mt * a.each + wg * hc;
-      uint64_t acc[64];
+      if (walk0 < n_tiles && !scales()) return;
+      for (int w = walk0; w < n_tiles; w += n_walk) {
+        const int t0 = w % mt * 128 + (warp & 3) * 32, n0 = w / mt * BN + quarter * COLS;
+        uint64_t acc[COLS / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!mbar_wait_warp(&accfull[b], bph, abort_flag, a.status)) return;
-        tc_fence_after();
-        const uint32_t src = tlane + (uint32_t)(b * BN);
-        const uint64_t u = pack2(sc[0], sc[0]);
+        for (int i = 0; i < COLS / 2; ++i) acc[i] = 0;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait_warp(&accfull[b], bph, abort_flag, a.status)) return;
+          tc_fence_after();
+          const uint32_t src = tlane + (uint32_t)(b * BN);
+          const uint64_t u = pack2(sc[0], sc[0]);
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          uint64_t v[8];
-          tmem_get16x2(src + c, v);
-          if (c == 112) {   // all read: the next MMAs may have the columns
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&accfree[b]);
+          for (int c = 0; c < COLS; c += 16) {
+            uint64_t v[8];
+            tmem_get16x2(src + c, v);
+            if (c == COLS - 16) {   // all read: the next MMAs may have the columns
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&accfree[b]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[c / 2 + i] = fma2(v[i], u, acc[c / 2 + i]);
           }
+          b = (b + 1) & (NBUF - 1);
+          if (!b) bph ^= 1;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[c / 2 + i] = fma2(v[i], u, acc[c / 2 + i]);
+          for (int q = 0; q < 3; ++q) sc[q] = sc[q + 1];
+          if (kb + 1 == KB ? w + n_walk < n_tiles : (kb & 3) == 3)
+            if (!scales()) return;
         }
-        b ^= 1;
-        if (!b) bph ^= 1;
+        if (BN == 128 && a.split > 1) {
+          // This warp saw the CTA's last block: all copies and MMAs have
+          // completed, and the ring holds the sums now.
+          float* ex = reinterpret_cast<float*>(smem);   // [128 columns][128 rows]
 #pragma unroll
-        for (int q = 0; q < 3; ++q) sc[q] = sc[q + 1];
-        if (kb + 1 == KB ? w + n_walk < n_tiles : (kb & 3) == 3)
-          if (!scales()) return;
-      }
-      uint8_t* out = stage_out + warp * QR_OUT;
-      const int row0 = t - lane;
-      if (a.y_f32) {
+          for (int i = 0; i < COLS / 2; ++i) {
+            float u, v;
+            unpack2(acc[i], u, v);
+            ex[(quarter * COLS + 2 * i) * 128 + row] = u;
+            ex[(quarter * COLS + 2 * i + 1) * 128 + row] = v;
+          }
+          return;
+        }
+        uint8_t* out = stage_out + warp * QR_OUT;
+        const int step = a.y_f32 ? 16 : 32;
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          if (c < hc && n0 + c < a.n && row0 < a.T) {
+        for (int c = 0; c < COLS; c += 16) {
+          if ((c & (step - 1)) == 0 && n0 + c < a.n && t0 < a.T) {
             if (elect_one()) bulk_wait_read();
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {   // 16 bytes each, in the copy's 64-byte swizzle
-              float4 f;
-              unpack2(acc[c / 2 + 2 * i], f.x, f.y);
-              unpack2(acc[c / 2 + 2 * i + 1], f.z, f.w);
-              *reinterpret_cast<float4*>(out + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16) = f;
+              uint8_t* to = out + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16;
+              if (a.y_f32) {
+                float4 f;
+                unpack2(acc[c / 2 + 2 * i], f.x, f.y);
+                unpack2(acc[c / 2 + 2 * i + 1], f.z, f.w);
+                *reinterpret_cast<float4*>(to) = f;
+              } else if ((c & 31) == 0) {
+                float f[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) unpack2(acc[(c & ~31) / 2 + 4 * i + q], f[2 * q], f[2 * q + 1]);
+                store8_bf16(to, 0, f);
+              }
             }
-            store_rows(&mY, out, n0 + c, row0);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          if (c < hc && n0 + c < a.n && row0 < a.T) {
-            if (elect_one()) bulk_wait_read();
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float f[8];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) unpack2(acc[c / 2 + 4 * i + q], f[2 * q], f[2 * q + 1]);
-              store8_bf16(out + lane * 64 + ((i ^ (lane >> 1)) & 3) * 16, 0, f);
-            }
-            store_rows(&mY, out, n0 + c, row0);
+            store_rows(&mY, out, n0 + c, t0);
           }
         }
       }
-    }
     };
     run();
     __syncwarp();
@@ -635,14 +640,28 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
   }
   __syncwarp();
   tc_fence_before();
+  if (BN == 128 && a.split > 1) {
+    cluster_sync();   // every CTA's sums are in its ring
+    // CTA `rank` adds up and stores its part of every warp's 32 columns
+    const int each = 32 / a.split, c0 = (warp >> 2) * 32 + rank * each;
+    const int row = (warp & 3) * 32 + lane, t = walk0 % mt * 128 + row, n0 = walk0 / mt * BN + c0;
+    if (warp < QR_EPI_WARPS && t < a.T && !*abort_flag)
+      for (int c = 0; c < each; c += 4) {
+        if (n0 + c >= a.n) break;       // n is a multiple of 8
+        float v[4];
+        cluster_sums<4>(smem_u32(smem) + (uint32_t)((c0 + c) * 128 + row) * 4, 512, a.split, v);
+        const size_t at = ((size_t)t * a.n + n0 + c) / 4;
+        if (a.y_f32) reinterpret_cast<float4*>(a.y)[at] = make_float4(v[0], v[1], v[2], v[3]);
+        else reinterpret_cast<uint2*>(a.y)[at] = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      }
+    __syncwarp();
+    cluster_sync();   // nobody leaves while its sums are read
+  }
   __syncthreads();
-  // every MMA of the pair is complete before TMEM is freed
-  if (warp == QR_MMA) mbar_wait_warp(mma_done, 0, abort_flag, a.status);
-  __syncwarp();
-  if (CTAS == 2) cluster_sync();   // neither CTA leaves while the other may still signal or read it
   if (warp == QR_MMA) {
+    mbar_wait_warp(mma_done, 0, abort_flag, a.status);   // every MMA is complete before TMEM is freed
     tc_fence_after();
-    pair_tmem_dealloc<CTAS>(tmem, 512);
+    tmem_dealloc(tmem, 512);
   }
 }
 

@@ -55,7 +55,8 @@ def test_random_codes(T, k, n, out):
 @pytest.mark.parametrize("T,k,n", SHAPES)
 def test_exact_sums(T, k, n):
     # codes in -3..3 and scales 2^-2..2^2: every partial sum is a multiple of 2^-4 below 9 · 16 · 14336 < 2^21,
-    # 25 bits at most with sums that stay far below that bound: fp32 holds all of them exactly and any order of additions gives the same sum
+    # 25 bits at most with sums that stay far below that bound: fp32 holds all of them exactly and any order of additions
+    # gives the same sum
     xq, Wq = ints(3, T, k, lim=3, dtype=F32).to(F8), ints(4, n, k, lim=3, dtype=F32).to(F8)
     xs = torch.exp2(torch.randint(-2, 3, (T, groups(k)), generator=gen(5)).float()).cuda()
     Ws = torch.exp2(torch.randint(-2, 3, (groups(n), groups(k)), generator=gen(6)).float()).cuda()
@@ -135,3 +136,27 @@ def test_weight_blocks_of_zeros_and_large_scales():
     xq, xs = quantize_rows(randn(18, 5, 512, dtype=BF))
     check(op, xq, xs, "fp32")
     check(Fp8Linear(op.Wq, op.Ws * 2.0 ** 60), xq, xs * 2.0 ** -70, "fp32")
+
+
+# long k and few tiles of 128 x 128: 3, 1, 1, 18, 26, 63 and 112 of them, k cut in up to eight parts, also uneven ones
+LONG = [(33, 4096, 264), (128, 4112, 128), (100, 14336, 8), (300, 4240, 648), (200, 4240, 1544), (257, 6160, 2568),
+        (448, 6160, 3584)]
+
+
+@pytest.mark.parametrize("T,k,n", LONG)
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_long_inner_sizes(T, k, n, out):
+    test_random_codes(T, k, n, out)
+    test_exact_sums(T, k, n)
+
+
+@pytest.mark.parametrize("T,k,n", LONG[:5])
+def test_long_inner_sizes_leave_what_lies_behind_y(T, k, n):
+    op = Fp8Linear.from_weight(randn(20, n, k, dtype=BF, scale=k ** -0.5))
+    xq, xs = quantize_rows(randn(21, T, k, dtype=BF))
+    for dt, out in ((BF, "bf16"), (F32, "fp32")):
+        buf = torch.full((T + 3, n), 7.0, dtype=dt, device="cuda")
+        y = op.forward(xq, xs, out=out)
+        assert torch.equal(op.forward(xq, xs, out=out, y=buf[:T]), y)
+        assert (buf[T:] == 7).all()
+        assert all(torch.equal(op.forward(xq, xs, out=out), y) for _ in range(5))
