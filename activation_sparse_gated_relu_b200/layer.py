@@ -87,6 +87,10 @@ def _apart_or_in_place(out, name: str, *inputs) -> None:
             _apart(out, name, t)
 
 
+def _moved(name: str) -> None:
+    raise ValueError(f"{name}'s storage was replaced after the operator was made: make it anew")
+
+
 def _out_type(out: str):
     if out not in _OUT:
         raise ValueError(f"out must be one of {sorted(_OUT)}, got {out!r}")
@@ -159,6 +163,8 @@ class RmsNorm:
         self._ptr = ptr
 
     def _descriptor(self, x, residual, y):
+        if self.weight.data_ptr() != self._ptr:
+            _moved("weight")
         key = (x, residual, y)
         d = self._desc.get(key)
         if d is None:
@@ -269,6 +275,7 @@ def quantize_rows(x, *, codes=None, scale=None, stream: Optional[int] = None):
     T, d = _matrix(x, "x")
     dev = x.get_device() if x.is_cuda else None
     xp = _check(x, "x", (_BF16, _FP32), (T, d), dev)
+    given = codes is not None or scale is not None
     with _where(dev, stream):
         if codes is None:
             codes = torch.empty_like(x, dtype=_FP8)
@@ -276,6 +283,9 @@ def quantize_rows(x, *, codes=None, scale=None, stream: Optional[int] = None):
             scale = x.new_empty((T, _groups(d)), dtype=_FP32)
         qp = _check(codes, "codes", (_FP8,), (T, d), dev)
         cp = _check(scale, "scale", (_FP32,), (T, _groups(d)), dev)
+        if given:
+            _apart(codes, "codes", x, scale)
+            _apart(scale, "scale", x)
         _ok(load_library().sffn_quantize_rows(xp, _CODE[x.dtype], T, d, qp, cp, _raw_stream(dev)), "quantize_rows")
     return codes, scale
 
@@ -286,6 +296,7 @@ def quantize_blocks(W, *, codes=None, scale=None, stream: Optional[int] = None):
     n, k = _matrix(W, "W")
     dev = W.get_device() if W.is_cuda else None
     wp = _check(W, "W", (_BF16, _FP32), (n, k), dev)
+    given = codes is not None or scale is not None
     with _where(dev, stream):
         if codes is None:
             codes = torch.empty((n, k), dtype=_FP8, device=W.device)
@@ -293,13 +304,17 @@ def quantize_blocks(W, *, codes=None, scale=None, stream: Optional[int] = None):
             scale = torch.empty((_groups(n), _groups(k)), dtype=_FP32, device=W.device)
         qp = _check(codes, "codes", (_FP8,), (n, k), dev)
         cp = _check(scale, "scale", (_FP32,), (_groups(n), _groups(k)), dev)
+        if given:
+            _apart(codes, "codes", W, scale)
+            _apart(scale, "scale", W)
         _ok(load_library().sffn_quantize_blocks(wp, _CODE[W.dtype], n, k, qp, cp, _raw_stream(dev)),
             "quantize_blocks")
     return codes, scale
 
 
 class _Handle:
-    """A library handle that belongs to one device."""
+    """A library handle that belongs to one device.  It has to outlive the
+    graphs that its calls were captured into, as its weights have to."""
     _name = ""
 
     def _create(self, desc, stream: Optional[int]) -> None:
@@ -341,6 +356,7 @@ class Fp8Linear(_Handle):
         self.device = Wq.get_device()
         cp = _check(Ws, "Ws", (_FP32,), (_groups(n), _groups(k)), self.device)
         self.d_in, self.d_out, self.Wq, self.Ws = k, n, Wq, Ws
+        self._wp, self._cp = wp, cp
         self._create(sffn_qlinear_desc(d_in=k, d_out=n, Wq=wp, Ws=cp), stream)
         self._call, self._call_values = self._lib.sffn_qlinear_forward, self._lib.sffn_qlinear_quantize_forward
 
@@ -356,6 +372,8 @@ class Fp8Linear(_Handle):
         T, _ = _matrix(x, "x")
         dev, k = self.device, self.d_in
         dtype = _out_type(out)
+        if self.Wq.data_ptr() != self._wp or self.Ws.data_ptr() != self._cp:
+            _moved("Wq or Ws")
         codes = scale is not None
         xp = _check(x, "x", (_FP8,) if codes else _VALUES, (T, k), dev)
         if codes:
@@ -402,12 +420,14 @@ class GroupedLinear(_Handle):
         E, n, k = W.shape
         wp = _check(W, "W", (_BF16,), (E, n, k), None)
         self.device = W.get_device()
-        self.n_experts, self.d_out, self.d_in, self.W = E, n, k, W
+        self.n_experts, self.d_out, self.d_in, self.W, self._wp = E, n, k, W, wp
         self._create(sffn_grouped_desc(n_experts=E, d_in=k, d_out=n, W=wp), stream)
 
     def _rows(self, t, name: str, cols: int, offsets):
         R, _ = _matrix(t, name)
         p = _check(t, name, (_BF16,), (R, cols), self.device)
+        if self.W.data_ptr() != self._wp:
+            _moved("W")
         if not (isinstance(offsets, torch.Tensor) and offsets.dtype is torch.int32 and offsets.is_cuda
                 and offsets.get_device() == self.device and offsets.shape == (self.n_experts + 1,)
                 and offsets.is_contiguous()):

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from activation_sparse_gated_relu_b200 import (SFFN_OK, Fp8Linear, GroupedLinear, MoeFFN, RmsNorm, SparseFFN,
-                                               quantize_rows)
+                                               quantize_blocks, quantize_rows)
 from layer_util import HALF, U, check_codes, groups, randn, spread_cols, within
 
 pytestmark = pytest.mark.gpu
@@ -137,3 +137,37 @@ def test_classes_refuse():
         grp.backward(xb, xb[:4], off)
     with pytest.raises(RuntimeError):
         GroupedLinear(randn(66, 2, 12, 128, dtype=BF))
+
+
+def test_quantisers_refuse_overlapping_outputs():
+    x = torch.zeros(64, 256, dtype=torch.bfloat16, device="cuda")
+    bytes_ = x.view(torch.uint8).flatten()
+    over = bytes_[:64 * 256].view(torch.float8_e4m3fn).view(64, 256)
+    codes = torch.zeros(64, 256, dtype=torch.float8_e4m3fn, device="cuda")
+    inside = codes.view(torch.uint8).flatten()
+    with pytest.raises(ValueError, match="overlap"):
+        quantize_rows(x, codes=over)
+    with pytest.raises(ValueError, match="overlap"):
+        quantize_rows(x, codes=codes, scale=inside[:64 * 8].view(torch.float32).view(64, 2))
+    with pytest.raises(ValueError, match="overlap"):
+        quantize_rows(x, scale=bytes_[:64 * 8].view(torch.float32).view(64, 2))
+    with pytest.raises(ValueError, match="overlap"):
+        quantize_blocks(x, codes=over)
+    with pytest.raises(ValueError, match="overlap"):
+        quantize_blocks(x, codes=codes, scale=inside[:8].view(torch.float32).view(1, 2))
+
+
+def test_a_replaced_weight_is_noticed():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    norm = RmsNorm(torch.ones(256, dtype=torch.bfloat16, device="cuda"))
+    lin = Fp8Linear.from_weight(torch.ones(64, 256, dtype=torch.bfloat16, device="cuda"))
+    experts = GroupedLinear(torch.ones(2, 64, 256, dtype=torch.bfloat16, device="cuda"))
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    norm.forward(x), lin(x), experts(x, off)
+    for owner, name in ((norm, "weight"), (lin, "Wq"), (experts, "W")):
+        t = getattr(owner, name)
+        t.data = t.clone()
+    for call in (lambda: norm.forward(x), lambda: norm.backward(x, x), lambda: lin(x), lambda: experts(x, off),
+                 lambda: experts.backward(x, x[:, :64].contiguous(), off)):
+        with pytest.raises(ValueError, match="replaced"):
+            call()
