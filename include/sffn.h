@@ -504,7 +504,8 @@ sffn_status sffn_moe_timing_end(sffn_moe_handle* h, int max_kernels, char (*name
  * in the residual's type and may be the residual itself (NULL iff residual is
  * NULL); weight [d] bf16 or fp32; y [T][d] bf16, fp32, or e4m3 codes with
  * scale [T][ceil(d/128)], one for each 128 columns (scale is NULL for the other
- * types).  eps finite, >= 0.
+ * types).  eps finite, >= 0.  Sums of squares are fp32: they overflow (y = 0)
+ * where |s| passes about 1e19 / sqrt(d).
  * Limits: d % 8 == 0, d <= 16384 (SFFN_ERR_UNSUPPORTED). */
 typedef struct sffn_rmsnorm_desc {
   int d;
