@@ -75,22 +75,32 @@ namespace {
 
 struct NormShape {
   int tpr, nv, threads, rpc;   // threads per row, vectors per thread, threads and rows per CTA
+  int shift;                   // thread index >> shift: row within the CTA
 };
 
 NormShape norm_shape(int d) {
   NormShape s;
   const int dv = d / 8;
-  s.tpr = 32;
-  while (s.tpr < dv && s.tpr < 512) s.tpr *= 2;
-  s.nv = cdiv(dv, s.tpr);
-  s.nv = s.nv > 2 ? 4 : s.nv;
-  s.threads = std::max(s.tpr, 256);
+  if (dv <= 128) {
+    s.nv = 1;
+    s.shift = dv <= 32 ? 5 : dv <= 64 ? 6 : 7;
+    s.tpr = 1 << s.shift;
+    s.threads = 256;
+  } else {
+    s.nv = dv <= 512 ? 1 : dv <= 1024 ? 2 : 4;
+    s.shift = 10;
+    s.tpr = s.threads = cdiv(cdiv(dv, s.nv), 32) * 32;
+  }
   s.rpc = s.threads / s.tpr;
   return s;
 }
 
-constexpr int kNormBwdCtas = 296;
-int norm_bwd_ctas(const NormShape& s, int T) { return std::min(cdiv(T, s.rpc), kNormBwdCtas); }
+// CTAs of the gradient: as many as the SMs' registers hold, at most four an SM,
+// since each leaves a partial sum of dw; with T and d alone, for the workspace.
+int norm_bwd_ctas(const NormShape& s, int T, int per_sm) {
+  const int most = s.nv == 4 ? 1 : std::min(4, 1024 / s.threads);
+  return std::min(cdiv(T, s.rpc), 148 * std::min(most, per_sm));
+}
 
 sffn_status norm_validate(const sffn_rmsnorm_desc* d) {
   if (!d || !d->weight || !aligned16(d->weight)) return SFFN_ERR_INVALID_ARG;
@@ -125,8 +135,9 @@ cudaError_t norm_launch_res(int res, int out, const NormArgs& a, const NormShape
 }
 
 template <bool SF32, bool DYF32, bool DS, int NV>
-cudaError_t norm_bwd_launch_nv(const NormBwdArgs& a, const NormShape& s, int ctas, cudaStream_t st) {
+cudaError_t norm_bwd_launch_nv(const NormBwdArgs& a, const NormShape& s, int& ctas, cudaStream_t st) {
   const int smem = NormBwdCfg<SF32, DYF32, DS, NV>::smem(s.threads);
+  ctas = norm_bwd_ctas(s, a.T, 227 * 1024 / (smem + 2048));
   const auto kernel = k_rmsnorm_bwd<SF32, DYF32, DS, NV>;
   // set on every call: it belongs to the current device, and costs little
   const cudaError_t e =
@@ -138,7 +149,7 @@ cudaError_t norm_bwd_launch_nv(const NormBwdArgs& a, const NormShape& s, int cta
   return launch_pdl(kernel, dim3(ctas), dim3(s.threads), (size_t)smem, st, 1, a);
 }
 template <bool SF32, bool DYF32, bool DS>
-cudaError_t norm_bwd_launch(const NormBwdArgs& a, const NormShape& s, int ctas, cudaStream_t st) {
+cudaError_t norm_bwd_launch(const NormBwdArgs& a, const NormShape& s, int& ctas, cudaStream_t st) {
   switch (s.nv) {
     case 1: return norm_bwd_launch_nv<SF32, DYF32, DS, 1>(a, s, ctas, st);
     case 2: return norm_bwd_launch_nv<SF32, DYF32, DS, 2>(a, s, ctas, st);
@@ -146,7 +157,7 @@ cudaError_t norm_bwd_launch(const NormBwdArgs& a, const NormShape& s, int ctas, 
   }
 }
 template <bool SF32, bool DYF32>
-cudaError_t norm_bwd_launch_ds(const NormBwdArgs& a, const NormShape& s, int ctas, cudaStream_t st) {
+cudaError_t norm_bwd_launch_ds(const NormBwdArgs& a, const NormShape& s, int& ctas, cudaStream_t st) {
   return a.ds ? norm_bwd_launch<SF32, DYF32, true>(a, s, ctas, st) : norm_bwd_launch<SF32, DYF32, false>(a, s, ctas, st);
 }
 
@@ -175,6 +186,8 @@ extern "C" sffn_status sffn_rmsnorm_forward(const sffn_rmsnorm_desc* desc, const
   a.eps = desc->eps;
   const NormShape s = norm_shape(desc->d);
   a.tpr = s.tpr;
+  a.shift = s.shift;
+  a.rpc = s.rpc;
   const int res = !residual ? 0 : desc->residual_dtype == SFFN_FP32 ? 2 : 1;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   return launched(desc->x_dtype == SFFN_FP32 ? norm_launch_res<true>(res, desc->y_dtype, a, s, st)
@@ -185,7 +198,7 @@ extern "C" sffn_status sffn_rmsnorm_workspace_bytes(int d, int T, size_t* bytes)
   if (!bytes || d <= 0 || T < 0 || T > kMaxRows) return SFFN_ERR_INVALID_ARG;
   if (d % 8 || d > NORM_MAX_D) return SFFN_ERR_UNSUPPORTED;
   const NormShape s = norm_shape(d);
-  *bytes = (size_t)norm_bwd_ctas(s, T) * s.rpc * d * sizeof(float);
+  *bytes = (size_t)norm_bwd_ctas(s, T, 4) * d * sizeof(float);
   return SFFN_OK;
 }
 
@@ -203,7 +216,7 @@ extern "C" sffn_status sffn_rmsnorm_backward(const sffn_rmsnorm_desc* desc, cons
   if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return SFFN_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const NormShape s = norm_shape(desc->d);
-  const int ctas = norm_bwd_ctas(s, T);
+  int ctas = 0;   // as launched
   NormBwdArgs a{};
   a.dy = dy;
   a.s = s_in;
@@ -214,6 +227,8 @@ extern "C" sffn_status sffn_rmsnorm_backward(const sffn_rmsnorm_desc* desc, cons
   a.T = T;
   a.d = desc->d;
   a.tpr = s.tpr;
+  a.shift = s.shift;
+  a.rpc = s.rpc;
   a.w_f32 = desc->weight_dtype == SFFN_FP32;
   a.eps = desc->eps;
   cudaError_t e = cudaSuccess;
@@ -223,7 +238,7 @@ extern "C" sffn_status sffn_rmsnorm_backward(const sffn_rmsnorm_desc* desc, cons
            : (yf ? norm_bwd_launch_ds<false, true>(a, s, ctas, st) : norm_bwd_launch_ds<false, false>(a, s, ctas, st));
   }
   e = e ? e
-        : launch_pdl(k_rmsnorm_dw, dim3(cdiv(desc->d, 32)), dim3(512), 0, st, 1, (const float*)workspace, ctas * s.rpc,
+        : launch_pdl(k_rmsnorm_dw, dim3(cdiv(desc->d, 32)), dim3(512), 0, st, 1, (const float*)workspace, ctas,
                      desc->d, dweight);
   return launched(e);
 }

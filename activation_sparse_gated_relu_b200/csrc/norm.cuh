@@ -13,15 +13,17 @@
 // The sum of squares is an fp32 sum: |s| has to stay below about 1e19 / sqrt(d).
 //
 // Both are bound by memory: each value is read once and each result written
-// once.  Forward, 4096 rows of 2048, fp32 x, bf16 residual, sum and y (84 MB):
-// 13.4 us, 6.3 TB/s; 32 to 512 threads per row measured alike on long inputs
-// (43.1 to 43.2 us at 16384 x 2048), and the most are taken, which is quickest on
-// a few rows.  Gradient, 8191 rows of 4096, all bf16 (268 MB): 51.3 us, 5.2 TB/s,
-// and 3.6 for dw's partial sums.  A row is held in the registers of a group of TPR threads (a power of
-// two of 32 to 512, eight columns each, NV times), so that neither the second
-// use of s nor the 8-bit scale reads anything again; groups of fewer than 256
-// threads share a CTA.  Sums are fp32, in a fixed order.
+// once.  A row is held by a group of threads, eight columns each, once, twice or
+// four times: up to 1024 columns 32, 64 or 128 threads, several groups a CTA of
+// 256; above that a CTA of as many warps as the row needs, so that neither the
+// second use of s nor the 8-bit scale reads global memory again.  Forward, 4096
+// rows of 2048, fp32 x, bf16 residual, sum and y (84 MB): 12.7 us, 6.6 TB/s; 6213
+// rows of 5400 51 us, 6.5 TB/s (62 with groups of a power of two).  Gradient, 8191
+// rows of 4096, all bf16 (268 MB): 49.1 us, 5.5 TB/s, and 3.7 for dw's partial
+// sums.  Sums are fp32, in a fixed order.
 #pragma once
+
+#include <type_traits>
 
 #include "ptx_pair.cuh"
 #include "vec8.cuh"
@@ -37,7 +39,8 @@ struct NormArgs {
   void* s;             // the sum, in the residual's type (null without one)
   void* y;
   float* scale;        // [T][ceil(d/128)] with e4m3 output
-  int T, d, tpr, w_f32;
+  int T, d, w_f32;
+  int tpr, shift, rpc; // threads per row; thread index >> shift: row within the CTA; rows per CTA
   float eps;
 };
 
@@ -54,23 +57,23 @@ __device__ __forceinline__ void load_w8(const void* w, int w_f32, int vec, float
 }
 
 // Sums of v[0..N) over the row's threads (the same in all of them): warp sums to
-// shared memory, then every warp adds its row's, a power of two, in pairs.
+// shared memory, then every warp adds its row's, from warp `first` on, in pairs.
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[16], int warps_per_row) {
+__device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[16], int first, int warps_per_row) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
   if (warps_per_row == 1) return;
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) red[i][warp] = v[i];
   __syncthreads();
-  const int lane = threadIdx.x & 31, w = warp / warps_per_row * warps_per_row + (lane & (warps_per_row - 1));
+  const int n = 1 << (32 - __clz(warps_per_row - 1)), w = lane & (n - 1);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = red[i][w];
-  for (int o = warps_per_row >> 1; o > 0; o >>= 1)
+  for (int i = 0; i < N; ++i) v[i] = w < warps_per_row ? red[i][first + w] : 0.0f;
+  for (int o = n >> 1; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
 }
@@ -79,8 +82,8 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[16], int war
 template <bool XF32, int RES, int OUT, int NV>
 __global__ void __launch_bounds__(512) k_rmsnorm(const NormArgs a) {
   __shared__ float red[1][16];
-  const int tid = threadIdx.x & (a.tpr - 1);
-  const long long t = (long long)blockIdx.x * (blockDim.x / a.tpr) + threadIdx.x / a.tpr;
+  const int sub = threadIdx.x >> a.shift, tid = threadIdx.x & ((1 << a.shift) - 1);
+  const long long t = (long long)blockIdx.x * a.rpc + sub;
   const int dv = a.d / 8;
   griddep_wait();
   const bool row = t < a.T;
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm(const NormArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[0] += s[i][j] * s[i][j];
   }
-  row_sum<1>(sum, red, a.tpr >> 5);
+  row_sum<1>(sum, red, sub * (a.tpr >> 5), a.tpr >> 5);
   const float rstd = rsqrtf(sum[0] / (float)a.d + a.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -140,39 +143,41 @@ struct NormBwdArgs {
   const void* ds;      // or null
   const void* w;
   void* dx;            // in s's type
-  float* part;         // [gridDim.x · groups per CTA][d] partial sums of dw
-  int T, d, tpr, w_f32;
+  float* part;         // [gridDim.x][d] partial sums of dw
+  int T, d, w_f32;
+  int tpr, shift, rpc; // threads per row, as above, rows per CTA
   float eps;
 };
 
 // A row is a chain (load, two sums over its threads, gradient), so several
 // rows' values are on their way while one is worked on: every thread copies
-// its own eight columns of the rows to come into shared memory, STAGES rows
-// ahead, and reads them back itself, without any barrier.  Two CTAs an SM.
-// Where the rows are too wide for that (d > 8192 in fp32), STAGES is 0 and
-// they are loaded as they are needed.  What is left is bound by instruction
-// issue, so the arithmetic runs on pairs of columns.  Measured at 8191 x 4096:
-// rows loaded as they are needed, one column at a time 70.5 us, so 53.
+// its own columns of the rows to come into shared memory, STAGES - 1 rows
+// ahead, and reads them back itself, without any barrier, and again for their
+// second use.  That leaves 64 registers a thread enough up to 8192 columns, for
+// two CTAs of 512 threads an SM (four of 256).  Where the rows are too wide (d >
+// 8192 in fp32), STAGES is 0 and they are loaded as they are needed.  What is
+// left is bound by instruction issue, so the arithmetic runs on pairs of columns.
+// Measured at 8191 x 4096: rows loaded as they are needed, one column at a time
+// 70.5 us, so 49.1; at 4382 x 7656 the values in registers, one CTA, 82, so 63.
 template <bool SF32, bool DYF32, bool DS, int NV>
 struct NormBwdCfg {
   static constexpr int NS = SF32 ? 2 : 1, NY = DYF32 ? 2 : 1, ND = DS ? NS : 0;
   static constexpr int PER = (NS + NY + ND) * NV;              // 16-byte pieces per thread and row
-  static constexpr int STAGES = PER <= 3 ? 4 : PER <= 6 ? 4 : PER <= 12 ? 2 : 0;
+  static constexpr int STAGES = PER <= 3 ? 4 : PER <= 12 ? 2 : 0;
   static constexpr int smem(int threads) { return STAGES * PER * 16 * threads; }
 };
 
 // One group of threads takes rows g, g + groups, ... and keeps its part of dw
 // in registers over them.
 template <bool SF32, bool DYF32, bool DS, int NV>
-__global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) k_rmsnorm_bwd(const NormBwdArgs a) {
+__global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) k_rmsnorm_bwd(const NormBwdArgs a) {
   using Cfg = NormBwdCfg<SF32, DYF32, DS, NV>;
   constexpr int STAGES = Cfg::STAGES, NS = Cfg::NS, NY = Cfg::NY, ND = Cfg::ND;
   __shared__ float red[2][2][16];
   extern __shared__ uint4 ring[];      // [STAGES][PER][threads]
-  const int tid = threadIdx.x & (a.tpr - 1);
-  const int dv = a.d / 8;
-  const int rpc = blockDim.x / a.tpr;
-  const long long g = (long long)blockIdx.x * rpc + threadIdx.x / a.tpr;
+  const int sub = threadIdx.x >> a.shift, tid = threadIdx.x & ((1 << a.shift) - 1);
+  const int dv = a.d / 8, rpc = a.rpc;
+  const long long g = (long long)blockIdx.x * rpc + sub;
   const long long step = (long long)gridDim.x * rpc;
   griddep_wait();
   uint64_t dw[NV][4];
@@ -216,42 +221,34 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) k_rmsnorm_bwd(const Norm
   int par = 0, slot = 0;
   long long at_row = g * dv + tid;
   for (long long t0 = (long long)blockIdx.x * rpc; t0 < a.T; t0 += step, par ^= 1, at_row += step * dv) {
-    const long long t = t0 + threadIdx.x / a.tpr;
+    const long long t = t0 + sub;
     const bool row = t < a.T;
-    Raw8<SF32> rs[NV], rd[NV];
-    Raw8<DYF32> ry[NV];
     if (STAGES > 0) {
       ask(t + (STAGES - 1) * step, (slot + STAGES - 1) & (STAGES > 0 ? STAGES - 1 : 0));
       copies_wait<(STAGES > 0 ? STAGES - 1 : 0)>();
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    // this thread's i-th eight values of s, dy or ds: read from the ring as often
+    // as they are used, which leaves registers to a second CTA
+    auto get = [&](const void* base, auto f32, int i, int first, uint64_t (&f)[4]) {
+      Raw8<decltype(f32)::value> r;
+      r.zero();
       if (STAGES > 0) {
-        const uint4* from = ring + ((size_t)slot * Cfg::PER + i * (NS + NY + ND)) * blockDim.x + threadIdx.x;
+        const uint4* from = ring + ((size_t)slot * Cfg::PER + i * (NS + NY + ND) + first) * blockDim.x + threadIdx.x;
 #pragma unroll
-        for (int k = 0; k < NS; ++k) rs[i].v[k] = from[k * blockDim.x];
-#pragma unroll
-        for (int k = 0; k < NY; ++k) ry[i].v[k] = from[(NS + k) * blockDim.x];
-#pragma unroll
-        for (int k = 0; k < ND; ++k) rd[i].v[k] = from[(NS + NY + k) * blockDim.x];
-      } else {
-        rs[i].zero();
-        ry[i].zero();
-        rd[i].zero();
-        if (row && tid + i * a.tpr < dv) {
-          rs[i].load(a.s, at_row + i * a.tpr);
-          ry[i].load(a.dy, at_row + i * a.tpr);
-          if (DS) rd[i].load(a.ds, at_row + i * a.tpr);
-        }
+        for (int k = 0; k < (decltype(f32)::value ? 2 : 1); ++k) r.v[k] = from[k * blockDim.x];
+      } else if (row && tid + i * a.tpr < dv) {
+        r.load(base, at_row + i * a.tpr);
       }
-    }
-    if (STAGES > 0) slot = (slot + 1) & (STAGES - 1);
+      r.pairs(f);
+    };
+    const std::integral_constant<bool, SF32> sf;
+    const std::integral_constant<bool, DYF32> yf;
     uint64_t s0 = 0, s1 = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       uint64_t s[4], y[4], w[4];
-      rs[i].pairs(s);
-      ry[i].pairs(y);
+      get(a.s, sf, i, 0, s);
+      get(a.dy, yf, i, NS, y);
       if (NV > 1) weight(i, w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -264,15 +261,15 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) k_rmsnorm_bwd(const Norm
     sum[0] += hi;
     unpack2(s1, sum[1], hi);
     sum[1] += hi;
-    row_sum<2>(sum, red[par], a.tpr >> 5);
+    row_sum<2>(sum, red[par], sub * (a.tpr >> 5), a.tpr >> 5);
     const float rstd = rsqrtf(sum[0] / (float)a.d + a.eps);
     const float c = sum[1] * rstd * rstd * rstd / (float)a.d;
     const uint64_t r2 = pack2(rstd, rstd), c2 = pack2(-c, -c);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       uint64_t s[4], y[4], w[4], dx[4];
-      rs[i].pairs(s);
-      ry[i].pairs(y);
+      get(a.s, sf, i, 0, s);
+      get(a.dy, yf, i, NS, y);
       if (NV > 1) weight(i, w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -280,7 +277,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) k_rmsnorm_bwd(const Norm
         dw[i][j] = fma2(y[j], mul2(s[j], r2), dw[i][j]);   // rows past the end are zeros
       }
       if (DS) {
-        rd[i].pairs(s);
+        get(a.ds, sf, i, NS + NY, s);
 #pragma unroll
         for (int j = 0; j < 4; ++j) dx[j] = add2(dx[j], s[j]);
       }
@@ -292,15 +289,35 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) k_rmsnorm_bwd(const Norm
         else store8_bf16(a.dx, at_row + i * a.tpr, f);
       }
     }
+    if (STAGES > 0) slot = (slot + 1) & (STAGES - 1);
   }
   if (STAGES > 0) copies_wait<0>();
+  if (rpc > 1) {   // the CTA's groups, eight columns a thread, join in the ring's memory
+    static_assert(NV > 1 || STAGES * Cfg::PER * 16 >= 32, "a thread's eight sums");
+    float f[8], u[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpack2(dw[0][j], f[2 * j], f[2 * j + 1]);
+    __syncthreads();
+    store8_f32(ring, threadIdx.x, f);
+    __syncthreads();
+    if (sub > 0 || tid >= dv) return;
+    for (int k = 1; k < rpc; ++k) {
+      Raw8<true> r;
+      r.load(ring, threadIdx.x + k * a.tpr);
+      r.get(u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] += u[j];
+    }
+    store8_f32(a.part, (size_t)blockIdx.x * dv + tid, f);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = tid + i * a.tpr;
     float f[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) unpack2(dw[i][j], f[2 * j], f[2 * j + 1]);
-    if (v < dv) store8_f32(a.part, (size_t)g * dv + v, f);
+    if (v < dv) store8_f32(a.part, (size_t)blockIdx.x * dv + v, f);
   }
 }
 
