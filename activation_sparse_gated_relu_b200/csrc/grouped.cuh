@@ -22,6 +22,14 @@
 // Persistent CTAs (or CTA pairs: 256 rows, each CTA holding half of the
 // columns' operand) walk the tiles of all experts; two accumulators in TMEM
 // let the MMAs of a tile run beside the stores of the tile before.
+//
+// With many rows the tensor cores bound it: 8192 rows in 8 groups, 2048 to 8192,
+// forward 194 us (1.4 PFLOP/s, where the power limit holds the clock at about 1.5
+// GHz), input gradient 200; the weight gradient, whose 537 MB leave beside the
+// MMAs, 260 (207 without its stores).  With few rows the weights' bytes do: 16
+// rows in 8 groups, 4096 to 14336, 128 us (6.4 TB/s).  There a tile is 32 columns
+// and 128 rows m, and where tiles are fewer than SMs a cluster shares each tile's
+// k and adds the parts up through distributed shared memory, in a fixed order.
 #pragma once
 
 #include "ptx_pair.cuh"
@@ -60,6 +68,7 @@ struct GroupedArgs {
   int E, R;
   int M, N, K;          // rows m; columns c (weight gradient); inner size k (forward and input gradient)
   int out_f32;
+  int split;            // 32 columns: CTAs of a cluster, each with a part of k; one tile per cluster then
   int kchunk;           // k blocks that the tensor core adds up before they join the fp32 sum in registers
   uint32_t* status;
 };
@@ -95,11 +104,12 @@ template <int MODE, int CTAS, int BN>
 struct GtWalk {
   const int *ra, *rb, *first;   // group rows, first tile of each expert ([E] the total)
   int M, N, K, e;
+  int split, rank;              // this CTA's part of k
   // the current tile
   int m0;                       // first row m of the tile (of the pair)
   int c0, cols, bn;             // first column, columns stored, columns computed
   int krow;                     // weight gradient: first row of the group
-  int kbs, ktail;               // k blocks, and values in the last one
+  int kb0, kbs, ktail;          // first k block, k blocks, and values in the last one
   size_t orow;                  // output row of column 0
 
   __device__ __forceinline__ void set(int w) {
@@ -129,6 +139,13 @@ struct GtWalk {
       orow = (size_t)c0;
     }
     bn = (cols + STEP - 1) / STEP * STEP;
+    kb0 = 0;
+    if (BN == 32 && split > 1) {
+      const int all = kbs;
+      kb0 = all * rank / split;
+      kbs = all * (rank + 1) / split - kb0;
+      if (rank + 1 < split) ktail = GT_BK;
+    }
   }
 };
 
@@ -162,7 +179,8 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 ? cluster_rank() : 0u;
-  const int n_walk = gridDim.x / CTAS, walk0 = blockIdx.x / CTAS;
+  const int split = BN == 32 ? args.split : 1;
+  const int n_walk = gridDim.x / (CTAS * split), walk0 = blockIdx.x / (CTAS * split);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -237,6 +255,8 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   t.N = args.N;
   t.K = args.K;
   t.e = 0;
+  t.split = split;
+  t.rank = split > 1 ? (int)cluster_rank() : 0;
 
   if (warp == GT_PRODUCER) {
     // --------------------------------------------------------- TMA producer
@@ -260,7 +280,7 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
           if (tail) mbar_expect_tx(&tailbar[s], bytes);
           else if (CTAS == 2) mbar_expect_cluster(bar, bytes);
           else mbar_expect_tx(&full[s], bytes);
-          const int k0 = kb * GT_BK;
+          const int k0 = (t.kb0 + kb) * GT_BK;
           if (MODE == GROUPED_FWD) {
             tma_3d<CTAS>(sa, &mA, bar, k0, m0, t.e);
           } else if (MODE == GROUPED_DX) {
@@ -402,6 +422,13 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         }
       }
     };
+    // k shared by a cluster: this CTA's sums into the ring's memory, which the
+    // tile's last accumulator shows to be free
+    auto put = [&](const float (&v)[32]) {
+      float* ex = reinterpret_cast<float*>(smem) + (warp & 3) * 32 + lane;   // [32 columns][128 rows]
+#pragma unroll
+      for (int i = 0; i < 32; ++i) ex[i * 128] = v[i];
+    };
     // Left at once when a wait fails: leaving a loop from its middle would keep
     // both sides' sums alive, a select for each of them.
     auto run = [&]() {
@@ -431,7 +458,8 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
             float v[32];
             tmem_get32(tlane + (uint32_t)(b * BN + 64 * j), v);
             if (j == pieces - 1) release(b);
-            store(v, 64 * j + 32 * wg);
+            if (BN == 32 && split > 1) put(v);
+            else store(v, 64 * j + 32 * wg);
             __syncwarp();
           }
         } else {
@@ -461,7 +489,8 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
 #pragma unroll
           for (int j = 0; j < NCH; ++j)
             if (j < pieces) {
-              store(acc[j], 64 * j + 32 * wg);
+              if (BN == 32 && split > 1) put(acc[j]);
+              else store(acc[j], 64 * j + 32 * wg);
               __syncwarp();
             }
         }
@@ -471,6 +500,28 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   }
   __syncwarp();
   tc_fence_before();
+  if (BN == 32 && split > 1) {
+    cluster_sync();   // every CTA's sums are in its ring
+    if (walk0 < n_tiles && warp < GT_EPI_WARPS) {
+      // CTA `rank` adds up and stores every split-th column
+      t.set(walk0);
+      const int row = threadIdx.x & 127, m = t.m0 + row, step = 2 * split;
+      if (m < t.M && !*abort_flag)
+        for (int c = t.rank + split * (threadIdx.x >> 7); c < t.cols; c += 4 * step) {   // reads on to column 31 + 48
+          float v[4];
+          cluster_sums<4>(smem_u32(smem) + (uint32_t)(c * 128 + row) * 4, (uint32_t)step * 512, split, v);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const size_t at = (t.orow + c + step * q) * (size_t)t.M + m;
+            if (c + step * q >= t.cols) break;
+            if (args.out_f32) reinterpret_cast<float*>(args.out)[at] = v[q];
+            else reinterpret_cast<__nv_bfloat16*>(args.out)[at] = __float2bfloat16(v[q]);
+          }
+        }
+    }
+    __syncwarp();
+    cluster_sync();   // nobody leaves while its sums are read
+  }
   __syncthreads();
   // every MMA of this CTA (pair) is complete before TMEM is freed
   if (warp == GT_MMA) mbar_wait_warp(mma_done, 0, abort_flag, args.status);

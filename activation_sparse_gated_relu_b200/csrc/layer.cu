@@ -506,6 +506,7 @@ extern "C" sffn_status sffn_qlinear_destroy(sffn_qlinear_handle* h) {
 struct sffn_grouped_handle {
   sffn_grouped_desc desc;
   int dev = 0, n_sm = 0;
+  int slots[4] = {0, 0, 0, 0};  // clusters of 1, 2, 4 and 8 CTAs that the GPU holds at once, one CTA per SM
   uint32_t* status = nullptr;   // [4]
   CUtensorMap mW, mWT;          // W as the forward's (K-major) and the input gradient's (M-major) operand
 };
@@ -538,14 +539,15 @@ sffn_status grouped_launch(const sffn_grouped_handle* h, const CUtensorMap& mA, 
                            const GroupedArgs& g, long long tiles, cudaStream_t st) {
   CUtensorMap mB;
   if (!grouped_map(&mB, cols, inner, g.R, 0, MODE == GROUPED_DW ? 64 : GtCfg<CTAS, BN>::BOX)) return SFFN_ERR_CUDA;
-  const int grid = (int)std::min<long long>(tiles, h->n_sm / CTAS) * CTAS;
+  const int cluster = CTAS * g.split;
+  const int grid = (int)std::min<long long>(tiles, h->n_sm / CTAS) * cluster;   // a split has no more tiles than fit
   return launched(launch_pdl(k_grouped<MODE, CTAS, BN>, dim3(grid), dim3(GT_THREADS), (size_t)GtCfg<CTAS, BN>::SMEM, st,
-                             CTAS, mA, mB, g));
+                             cluster, mA, mB, g));
 }
 
 // Products over the rows of every group (forward, input gradient).
 template <int MODE>
-sffn_status grouped_rows(const sffn_grouped_handle* h, const CUtensorMap& mA, const void* rows, const GroupedArgs& g,
+sffn_status grouped_rows(const sffn_grouped_handle* h, const CUtensorMap& mA, const void* rows, GroupedArgs g,
                          cudaStream_t st) {
   const long long tiles = (long long)cdiv(g.M, 128) * (g.R / 32 + g.E);
   if (tiles > kMaxTiles) return SFFN_ERR_UNSUPPORTED;
@@ -561,7 +563,24 @@ sffn_status grouped_rows(const sffn_grouped_handle* h, const CUtensorMap& mA, co
   //     256                     |   126 49.7 43.1                     |   133 47.9 43.2
   if (g.R >= 112ll * g.E) return grouped_launch<MODE, 2, 256>(h, mA, rows, g.K, g, tiles, st);
   if (g.R >= (MODE == GROUPED_FWD ? 24ll : 8ll) * g.E) return grouped_launch<MODE, 1, 128>(h, mA, rows, g.K, g, tiles, st);
-  return grouped_launch<MODE, 1, 32>(h, mA, rows, g.K, g, tiles, st);
+  // A few rows: no more tiles than this, since no more groups have a row.  Where
+  // they leave SMs idle, clusters share a tile's k, by a model of the time in ns:
+  // a block of k takes 240, a sum over the cluster 3000.  Measured without and
+  // with: 2 rows of 14336 to 4096 57 and 32 us, 4 rows (of 4 groups) of 8192 to 2048
+  // 34 and 20.5, 1 row of 4096 to 1024 18.5 and 7.6.
+  const long long few = (long long)cdiv(g.M, 128) * (g.R / 32 + std::min(g.E, g.R));
+  const int kb = cdiv(g.K, GT_BK);
+  long long best = kb * 240ll;
+  for (int i = 1; i < 4; ++i) {
+    const int split = 1 << i;
+    if (few > h->slots[i] || kb < 4 * split) continue;
+    const long long cost = cdiv(kb, split) * 240ll + 3000;
+    if (cost < best) {
+      best = cost;
+      g.split = split;
+    }
+  }
+  return grouped_launch<MODE, 1, 32>(h, mA, rows, g.K, g, few, st);
 }
 
 }  // namespace
@@ -599,6 +618,8 @@ extern "C" sffn_status sffn_grouped_create(const sffn_grouped_desc* desc, void* 
   e = e ? e : grouped_attr<GROUPED_DX, 1, 128>();
   e = e ? e : grouped_attr<GROUPED_DX, 1, 32>();
   e = e ? e : grouped_attr<GROUPED_DW, 2, 256>();
+  h->slots[0] = n_sm;
+  e = e ? e : count_clusters(k_grouped<GROUPED_FWD, 1, 32>, GT_THREADS, GtCfg<1, 32>::SMEM, h->slots);
   e = e ? e : cudaStreamSynchronize(st);
   if (e) {
     cudaGetLastError();
@@ -631,6 +652,7 @@ GroupedArgs grouped_args(const sffn_grouped_handle* h, const int32_t* offsets, i
   g.E = h->desc.n_experts;
   g.R = R;
   g.out_f32 = out_dtype == SFFN_FP32;
+  g.split = 1;
   g.kchunk = g.out_f32 ? 8 : 1 << 30;
   g.status = h->status;
   return g;

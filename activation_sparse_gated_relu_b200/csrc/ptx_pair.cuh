@@ -249,4 +249,26 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t chun
   return d;
 }
 
+// v[q] = the sum over the cluster's CTAs, in order, of their shared memory's
+// float at addr + q · step.  All loads go out before the first sum.
+template <int N>
+__device__ __forceinline__ void cluster_sums(uint32_t addr, uint32_t step, int split, float (&v)[N]) {
+  float u[8][N];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (r < split) {
+      const uint32_t from = cluster_addr(addr, (uint32_t)r);
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u[r][q]) : "r"(from + (uint32_t)q * step) : "memory");
+    }
+#pragma unroll
+  for (int q = 0; q < N; ++q) v[q] = 0.0f;
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (r < split)
+#pragma unroll
+      for (int q = 0; q < N; ++q) v[q] += u[r][q];
+}
+
 }  // namespace sffn

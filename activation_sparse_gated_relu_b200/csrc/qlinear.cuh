@@ -58,28 +58,6 @@ __device__ __forceinline__ void put_y(void* y, int f32, size_t at, float v) {
   else reinterpret_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16(v);
 }
 
-// v[q] = the sum over the cluster's CTAs, in order, of their shared memory's
-// float at addr + q · step.  All loads go out before the first sum.
-template <int N>
-__device__ __forceinline__ void cluster_sums(uint32_t addr, uint32_t step, int split, float (&v)[N]) {
-  float u[8][N];
-#pragma unroll
-  for (int r = 0; r < 8; ++r)
-    if (r < split) {
-      const uint32_t from = cluster_addr(addr, (uint32_t)r);
-#pragma unroll
-      for (int q = 0; q < N; ++q)
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u[r][q]) : "r"(from + (uint32_t)q * step) : "memory");
-    }
-#pragma unroll
-  for (int q = 0; q < N; ++q) v[q] = 0.0f;
-#pragma unroll
-  for (int r = 0; r < 8; ++r)
-    if (r < split)
-#pragma unroll
-      for (int q = 0; q < N; ++q) v[q] += u[r][q];
-}
-
 template <int BN>
 struct QcCfg {
   static constexpr int KS = 2;                           // 128-wide blocks per stage

@@ -217,3 +217,44 @@ def test_offsets_that_run_back_and_forth_count_no_row_twice():
     assert torch.equal(y, (x.float() @ op.W[0].float().t()).to(BF))
     assert torch.equal(g["dx"], (dy.float() @ op.W[0].float()).to(BF))
     assert torch.equal(g["dW"][0], dy.float().t() @ x.float()) and (g["dW"][1:] == 0).all()
+
+
+# few rows and a long inner size, whose parts the CTAs of a cluster take: forward in the first four, both in the
+# fifth, the input gradient in the last two; odd part lengths, short last blocks, groups of 32 and 33 rows
+FEW = [
+    ([1, 0, 1, 1], 0, 5, 3472, 920),
+    ([3], 2, 1, 2056, 136),
+    ([0, 2, 0, 33, 1], 1, 0, 4104, 264),
+    ([0] * 60 + [1, 0, 1, 0], 0, 0, 6152, 1032),
+    ([20, 3], 0, 2, 2056, 2120),
+    ([2, 0, 5], 0, 0, 264, 4104),
+    ([7], 0, 0, 128, 14336),
+]
+
+
+@pytest.mark.parametrize("counts,lead,tail,k,n", FEW)
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+def test_few_rows_and_long_sums(counts, lead, tail, k, n, out):
+    test_forward_and_gradients(counts, lead, tail, k, n, out)
+
+
+@pytest.mark.parametrize("counts,lead,tail,k,n", FEW[:5])
+def test_few_rows_are_exact_and_alike(counts, lead, tail, k, n):
+    # whole numbers up to 4: sums below 16 · 6152 < 2^24, exact in fp32
+    off, offsets = layout(counts, lead)
+    R = off[-1] + tail
+    x, W = ints(40, R, k), ints(41, len(counts), n, k)
+    x[off[-1]:] = float("nan")
+    x[:lead] = float("nan")
+    op = GroupedLinear(W)
+    ref = torch.cat([x[off[e]:off[e + 1]].double() @ W[e].double().t() for e in range(len(counts))])
+    rows = slice(lead, off[-1])
+    for _ in range(5):
+        assert torch.equal(op.forward(x, offsets, out="fp32")[rows], ref.float())
+        assert torch.equal(op.forward(x, offsets)[rows], ref.float().to(BF))
+    assert op.read_status() == SFFN_OK
+    # offsets that name other groups, or none, than the call before
+    none = torch.full_like(offsets, lead)
+    y = torch.full((R, n), 7.0, dtype=BF, device="cuda")
+    op.forward(x, none, y=y)
+    assert (y == 7).all() and op.read_status() == SFFN_OK
