@@ -153,8 +153,8 @@ class RmsNorm:
         ptr = _check(weight, "weight", (_BF16, _FP32), (self.d,), None)
         self.weight, self.eps, self.device = weight, float(eps), weight.get_device()
         self._lib = load_library()
-        self._call = self._lib.sffn_rmsnorm_forward
-        self._desc = {}
+        self._call, self._call_backward = self._lib.sffn_rmsnorm_forward, self._lib.sffn_rmsnorm_backward
+        self._desc, self._work, self._place = {}, {}, weight.device
         # refuse a size or an eps here rather than at the first call
         n = ctypes.c_size_t()
         _ok(self._lib.sffn_rmsnorm_workspace_bytes(self.d, 1, ctypes.byref(n)), "RmsNorm")
@@ -192,7 +192,7 @@ class RmsNorm:
             if residual is not None and residual_out is None:
                 residual_out = torch.empty_like(residual)
             if dtype is _FP8 and scale is None:
-                scale = x.new_empty((T, _groups(d)), dtype=_FP32)
+                scale = torch.empty((T, _groups(d)), dtype=_FP32, device=self._place)
             if given:
                 self._check_outputs(x, residual, dtype, y, scale, residual_out, shape)
             yp = y.data_ptr()
@@ -237,35 +237,43 @@ class RmsNorm:
         columns, as Fp8Linear takes them."""
         return self._forward(x, residual, _FP8, y, scale, residual_out, stream)
 
+    def _workspace(self, T: int) -> int:
+        n = ctypes.c_size_t()
+        _ok(self._lib.sffn_rmsnorm_workspace_bytes(self.d, T, ctypes.byref(n)), "RmsNorm.backward")
+        if len(self._work) < 1024:
+            self._work[T] = n.value
+        return n.value
+
     def backward(self, dy, s, ds=None, *, dx=None, dweight=None, stream: Optional[int] = None) -> dict:
         """{dx, dweight} for upstream dy (bf16 or fp32) and, if given, ds, the
         gradient that reaches s past the norm; dx has s's type, dweight is
         fp32 [d]."""
-        T, d = _matrix(s, "s")
+        T, _ = _matrix(s, "s")
         dev = self.device
         shape = (T, self.d)
         sp = _check(s, "s", (_BF16, _FP32), shape, dev)
         yp = _check(dy, "dy", (_BF16, _FP32), shape, dev)
         gp = None if ds is None else _check(ds, "ds", (s.dtype,), shape, dev)
-        n = ctypes.c_size_t()
-        _ok(self._lib.sffn_rmsnorm_workspace_bytes(d, T, ctypes.byref(n)), "RmsNorm.backward")
+        n = self._work.get(T) or self._workspace(T)
         with _where(dev, stream):
             if dweight is None:
-                dweight = torch.empty(self.d, dtype=_FP32, device=s.device)
+                dweight = torch.empty(self.d, dtype=_FP32, device=self._place)
                 wp = dweight.data_ptr()
             else:
                 wp = _check(dweight, "dweight", (_FP32,), (self.d,), dev)
                 _apart(dweight, "dweight", s, dy, self.weight, *(() if ds is None else (ds,)))
             if dx is None:
-                dx = torch.empty(shape, dtype=s.dtype, device=s.device)
+                dx = torch.empty_like(s)
                 xp = dx.data_ptr()
             else:
                 xp = _check(dx, "dx", (s.dtype,), shape, dev)
                 _apart_or_in_place(dx, "dx", s, dy, ds)
                 _apart(dx, "dx", self.weight, dweight)
-            work = torch.empty(n.value, dtype=torch.uint8, device=s.device)
-            _ok(self._lib.sffn_rmsnorm_backward(self._descriptor(_BF16, s.dtype, dy.dtype), yp, sp, gp, T, xp, wp,
-                                                work.data_ptr(), n.value, _raw_stream(dev)), "RmsNorm.backward")
+            work = torch.empty(n, dtype=torch.uint8, device=self._place)
+            e = self._call_backward(self._descriptor(_BF16, s.dtype, dy.dtype), yp, sp, gp, T, xp, wp, work.data_ptr(), n,
+                                    _raw_stream(dev))
+            if e:
+                raise SffnError(e, "RmsNorm.backward")
         return {"dx": dx, "dweight": dweight}
 
 
@@ -356,7 +364,7 @@ class Fp8Linear(_Handle):
         self.device = Wq.get_device()
         cp = _check(Ws, "Ws", (_FP32,), (_groups(n), _groups(k)), self.device)
         self.d_in, self.d_out, self.Wq, self.Ws = k, n, Wq, Ws
-        self._wp, self._cp = wp, cp
+        self._wp, self._cp, self._place = wp, cp, Wq.device
         self._create(sffn_qlinear_desc(d_in=k, d_out=n, Wq=wp, Ws=cp), stream)
         self._call, self._call_values = self._lib.sffn_qlinear_forward, self._lib.sffn_qlinear_quantize_forward
 
@@ -380,7 +388,7 @@ class Fp8Linear(_Handle):
             cp = _check(scale, "scale", (_FP32,), (T, _groups(k)), dev)
         with _where(dev, stream):
             if y is None:
-                y = x.new_empty((T, self.d_out), dtype=dtype)
+                y = torch.empty((T, self.d_out), dtype=dtype, device=self._place)
                 yp = y.data_ptr()
             else:
                 yp = _check(y, "y", (dtype,), (T, self.d_out), dev)
@@ -389,7 +397,7 @@ class Fp8Linear(_Handle):
                 s = self._call(self.h, xp, cp, T, yp, _CODE[dtype], _raw_stream(dev))
             else:
                 n = (T * k + 15) // 16 * 16 + 4 * T * _groups(k)
-                work = x.new_empty(n, dtype=torch.uint8)
+                work = torch.empty(n, dtype=torch.uint8, device=self._place)
                 s = self._call_values(self.h, xp, _CODE[x.dtype], T, yp, _CODE[dtype], work.data_ptr(), n,
                                       _raw_stream(dev))
             if s:
@@ -420,7 +428,8 @@ class GroupedLinear(_Handle):
         E, n, k = W.shape
         wp = _check(W, "W", (_BF16,), (E, n, k), None)
         self.device = W.get_device()
-        self.n_experts, self.d_out, self.d_in, self.W, self._wp = E, n, k, W, wp
+        self.n_experts, self.d_out, self.d_in, self.W = E, n, k, W
+        self._wp, self._place = wp, W.device
         self._create(sffn_grouped_desc(n_experts=E, d_in=k, d_out=n, W=wp), stream)
 
     def _rows(self, t, name: str, cols: int, offsets):
@@ -443,7 +452,7 @@ class GroupedLinear(_Handle):
         dev = self.device
         with _where(dev, stream):
             if y is None:
-                y = x.new_empty((R, self.d_out), dtype=dtype)
+                y = torch.empty((R, self.d_out), dtype=dtype, device=self._place)
                 yp = y.data_ptr()
             else:
                 yp = _check(y, "y", (dtype,), (R, self.d_out), dev)
