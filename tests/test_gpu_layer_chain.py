@@ -10,7 +10,7 @@ import torch
 
 from activation_sparse_gated_relu_b200 import (SFFN_OK, Fp8Linear, GroupedLinear, MoeFFN, RmsNorm, SparseFFN,
                                                quantize_blocks, quantize_rows)
-from layer_util import HALF, U, check_codes, groups, randn, spread_cols, within
+from layer_util import HALF, U, check_codes, groups, ints, randn, spread_cols, within
 
 pytestmark = pytest.mark.gpu
 
@@ -171,3 +171,38 @@ def test_a_replaced_weight_is_noticed():
                  lambda: experts.backward(x, x[:, :64].contiguous(), off)):
         with pytest.raises(ValueError, match="replaced"):
             call()
+
+
+def test_offsets_past_32_bits():
+    # 2^31 + 2^21 elements of 16 bits: the last rows against the same call on those rows alone (bit for bit, a row
+    # depends on no other), products of small whole numbers against their exact sums
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    T, d, last = 262400, 8192, slice(262400 - 130, 262400)
+    x = torch.empty(T, d, dtype=BF, device="cuda").fill_(0.5)
+    x[last] = randn(50, 130, d, dtype=BF)
+    norm = RmsNorm(randn(51, d, dtype=BF))
+    y, s = norm.forward(x, x)
+    y1, s1 = norm.forward(x[last].contiguous(), x[last].contiguous())
+    assert torch.equal(y[last], y1) and torch.equal(s[last], s1)
+    dx = norm.backward(y, s)["dx"]
+    assert torch.equal(dx[last], norm.backward(y1, s1)["dx"])
+    del s, dx
+    q, scale = quantize_rows(y)
+    q1, scale1 = quantize_rows(y1)
+    assert torch.equal(q[last].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(scale[last], scale1)
+    del q, y
+    W = ints(52, d, 64, lim=3)
+    small = ints(53, T, 64, lim=3)
+    ref = (small[last].float() @ W.float().t()).to(BF)     # below 9 · 64: exact in fp32
+    lin = Fp8Linear(W.to(torch.float8_e4m3fn), torch.ones(groups(d), 1, device="cuda"))
+    out = lin(small.to(torch.float8_e4m3fn), torch.ones(T, 1, device="cuda"))
+    assert torch.equal(out[last], ref) and lin.read_status() == SFFN_OK
+    op = GroupedLinear(torch.stack([-W, W]))
+    off = torch.tensor([0, 1000, T], dtype=torch.int32, device="cuda")
+    op.forward(small, off, y=out.zero_())
+    assert torch.equal(out[last], ref) and op.read_status() == SFFN_OK
+    dx = op.backward(small, x, off)["dx"]
+    within(dx[last], x[last].double() @ W.double(), (x[last].double() @ W.double()).abs() * HALF[BF]
+           + (d + 64) * U * (x[last].double().abs() @ W.double().abs()), "dx")
