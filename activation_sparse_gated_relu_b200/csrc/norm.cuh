@@ -262,7 +262,9 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) k_rmsnorm_bwd(const Norm
     unpack2(s1, sum[1], hi);
     sum[1] += hi;
     row_sum<2>(sum, red[par], sub * (a.tpr >> 5), a.tpr >> 5);
-    const float rstd = rsqrtf(sum[0] / (float)a.d + a.eps);
+    // rows past the end (with several rows a CTA) take any eps but 0, with which
+    // their zeros would give an infinity, and NaN in dw
+    const float rstd = rsqrtf(sum[0] / (float)a.d + (NV > 1 || row ? a.eps : 1.0f));
     const float c = sum[1] * rstd * rstd * rstd / (float)a.d;
     const uint64_t r2 = pack2(rstd, rstd), c2 = pack2(-c, -c);
 #pragma unroll
@@ -274,7 +276,7 @@ __global__ void __launch_bounds__(512, NV <= 2 ? 2 : 1) k_rmsnorm_bwd(const Norm
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         dx[j] = fma2(s[j], c2, mul2(mul2(y[j], NV == 1 ? w1[j] : w[j]), r2));
-        dw[i][j] = fma2(y[j], mul2(s[j], r2), dw[i][j]);   // rows past the end are zeros
+        dw[i][j] = fma2(y[j], mul2(s[j], r2), dw[i][j]);   // rows past the end add zeros
       }
       if (DS) {
         get(a.ds, sf, i, NS + NY, s);

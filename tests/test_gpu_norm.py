@@ -254,3 +254,23 @@ def test_quantize_nan_stays_in_its_element():
     assert torch.isnan(q[1, 200].float()) and torch.isfinite(c).all()
     assert torch.equal(q[0].view(torch.uint8), want_q[0].view(torch.uint8))
     assert torch.equal(q[1, :128].view(torch.uint8), want_q[1, :128].view(torch.uint8))
+
+
+@pytest.mark.parametrize("T", [1, 3, 13])
+@pytest.mark.parametrize("d", [8, 256, 264, 512, 1024, 1032])
+@pytest.mark.parametrize("st,yt,with_ds", [(BF, BF, True), (F32, BF, False), (BF, F32, False), (F32, F32, True)])
+def test_backward_without_eps(T, d, st, yt, with_ds):
+    # up to 1024 columns a CTA has 2, 4 or 8 rows' threads, some of them past the last row here: what
+    # they hold (zeros, whose norm is 0) reaches no sum.  Bounds as in test_backward.
+    s = randn(70, T, d, dtype=st, scale=1.5)
+    dy = randn(71, T, d, dtype=yt, scale=0.1)
+    ds = randn(72, T, d, dtype=st, scale=0.1) if with_ds else None
+    w = (1 + 0.2 * randn(73, d)).to(BF)
+    dx, dw, rstd, g = ref_backward(dy, s, ds, w, 0.0)
+    got = RmsNorm(w, 0.0).backward(dy, s, ds)
+    size = rstd * g.abs() + s.double().abs() * rstd ** 3 / d * (g * s.double()).abs().sum(1, keepdim=True)
+    tol = dx.abs() * HALF[st] + 160 * U * size
+    if ds is not None:
+        tol = tol + 4 * U * ds.double().abs()
+    within(got["dx"], dx, tol, "dx")
+    within(got["dweight"], dw, ((T / 8 + 400) * U + REL) * (dy.double() * s.double() * rstd).abs().sum(0) + 1e-38, "dweight")
