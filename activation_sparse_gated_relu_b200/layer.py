@@ -203,6 +203,8 @@ class RmsNorm:
             s = self._call(self._descriptor(x.dtype, rt, dtype), xp, rp, T, sp, yp, cp, _raw_stream(dev))
             if s:
                 raise SffnError(s, "RmsNorm.forward")
+        if residual is None and given and T and yp == xp:   # x holds y now
+            return y, scale, None
         return y, scale, residual_out if residual is not None else x
 
     def _check_outputs(self, x, residual, dtype, y, scale, residual_out, shape) -> None:
@@ -226,7 +228,8 @@ class RmsNorm:
     def forward(self, x, residual=None, *, out: str = "bf16", y=None, residual_out=None, stream: Optional[int] = None):
         """(y, s): x [T][d] bf16 or fp32, residual [T][d] bf16 or fp32 or None,
         y bf16 or fp32 by `out`, s in the residual's type (x itself without a
-        residual).  residual_out may be the residual."""
+        residual, or None where y replaces it).  residual_out may be the
+        residual, y x or the residual."""
         y, _, s = self._forward(x, residual, _out_type(out), y, None, residual_out, stream)
         return y, s
 

@@ -274,3 +274,21 @@ def test_backward_without_eps(T, d, st, yt, with_ds):
         tol = tol + 4 * U * ds.double().abs()
     within(got["dx"], dx, tol, "dx")
     within(got["dweight"], dw, ((T / 8 + 400) * U + REL) * (dy.double() * s.double() * rstd).abs().sum(0) + 1e-38, "dweight")
+
+
+def test_a_norm_in_place_gives_no_sum():
+    # without a residual the sum is x itself; where y replaces x, x holds it no longer
+    x, _, w = case(5, 264, BF, None, seed=80)
+    op = RmsNorm(w)
+    want, s = op(x)
+    assert s is x
+    other = torch.empty_like(x)
+    assert op(x, y=other)[1] is x and torch.equal(other, want)
+    for y in (x.clone(), x.clone()):
+        got, s = op(y, y=y.view(5, 264))
+        assert s is None and torch.equal(y, want) and got.data_ptr() == y.data_ptr()
+    r = randn(81, 5, 264, dtype=BF)
+    want, want_s = op(x, r)
+    xb = x.clone()
+    got, s = op(xb, r, y=xb)
+    assert torch.equal(got, want) and torch.equal(s, want_s)
