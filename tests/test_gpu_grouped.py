@@ -258,3 +258,37 @@ def test_few_rows_are_exact_and_alike(counts, lead, tail, k, n):
     y = torch.full((R, n), 7.0, dtype=BF, device="cuda")
     op.forward(x, none, y=y)
     assert (y == 7).all() and op.read_status() == SFFN_OK
+
+
+def _half_step(ref, eps_bits=8):
+    """Half of bf16's step in each value's own binade."""
+    return torch.exp2(torch.floor(torch.log2(ref.abs())) - eps_bits)
+
+
+@pytest.mark.parametrize("what", ["y", "dx", "dW"])
+def test_long_sums_into_bf16(what):
+    """Sums of 2^20 positive terms, rounded to bf16 once.  The tensor core adds 16 terms at a time to a sum of 24 bits
+    and drops what lies below, less than 2^-22 of the sum (its own last bit and the terms'); runs of 16384 terms are 1024
+    such steps, 2^-12 at most, and 64 runs added in fp32 at most 64 U more.  Columns of different sizes, so that the
+    sums lie all over a binade."""
+    K = 1 << 20
+    size = torch.linspace(1, 2, 64, device="cuda")
+    a = (1 + torch.rand(K, 64, generator=torch.Generator("cuda").manual_seed(50), device="cuda")) * size
+    b = 1 + torch.rand(K, 24, generator=torch.Generator("cuda").manual_seed(51), device="cuda")
+    a, b = a.to(BF), b.to(BF)
+    if what == "dW":
+        op = GroupedLinear(torch.zeros(1, 24, 64, dtype=BF, device="cuda"))
+        dW = torch.empty(1, 24, 64, dtype=BF, device="cuda")
+        op.backward(a, b, torch.tensor([0, K], dtype=torch.int32, device="cuda"), dW=dW)
+        got = dW[0]
+    else:
+        off = torch.tensor([0, 24], dtype=torch.int32, device="cuda")
+        if what == "y":
+            op = GroupedLinear(a.t().contiguous()[None])
+            got = op.forward(b.t().contiguous(), off)
+        else:
+            op = GroupedLinear(a[None])
+            got = op.backward(torch.zeros(24, 64, dtype=BF, device="cuda"), b.t().contiguous(), off)["dx"]
+    ref = b.double().t() @ a.double()
+    within(got, ref, _half_step(ref) + ref * (2.0 ** -12 + 64 * U), what)
+    assert op.read_status() == SFFN_OK
