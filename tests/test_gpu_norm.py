@@ -292,3 +292,11 @@ def test_a_norm_in_place_gives_no_sum():
     xb = x.clone()
     got, s = op(xb, r, y=xb)
     assert torch.equal(got, want) and torch.equal(s, want_s)
+
+
+@pytest.mark.parametrize("T,d", [(1500, 4104), (1500, 8192), (700, 12296), (700, 16384)])
+@pytest.mark.parametrize("st", [BF, F32])
+@pytest.mark.parametrize("yt", [BF, F32])
+@pytest.mark.parametrize("with_ds", [False, True])
+def test_backward_with_several_rows_per_cta(T, d, st, yt, with_ds):
+    test_backward(T, d, st, yt, with_ds)
