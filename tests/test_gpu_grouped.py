@@ -292,3 +292,29 @@ def test_long_sums_into_bf16(what):
     ref = b.double().t() @ a.double()
     within(got, ref, _half_step(ref) + ref * (2.0 ** -12 + 64 * U), what)
     assert op.read_status() == SFFN_OK
+
+
+def test_gradients_of_the_operator_against_differences():
+    # whole numbers up to 4: L = sum(y·dy) is exact, and linear in x and in W, so that a difference over a step of 2
+    # is the gradient's very value
+    counts, k, n = [3, 0, 2], 16, 24
+    off, offsets = layout(counts, 1)
+    R = off[-1] + 2
+    x, dy, W = ints(60, R, k), ints(61, R, n), ints(62, 3, n, k)
+    mine = slice(off[0], off[-1])
+    got = GroupedLinear(W).backward(x, dy, offsets, out="fp32")
+
+    def loss(x, W):
+        y = GroupedLinear(W).forward(x, offsets, out="fp32")
+        return (y[mine].double() * dy[mine].double()).sum().item()
+
+    for r, c in ((1, 0), (3, 15), (4, 7), (5, 9)):
+        up, down = x.clone(), x.clone()
+        up[r, c] += 1
+        down[r, c] -= 1
+        assert (loss(up, W) - loss(down, W)) / 2 == got["dx"][r, c].item()
+    for e, o, c in ((0, 3, 2), (0, 23, 15), (1, 0, 0), (2, 15, 7)):
+        up, down = W.clone(), W.clone()
+        up[e, o, c] += 1
+        down[e, o, c] -= 1
+        assert (loss(x, up) - loss(x, down)) / 2 == got["dW"][e, o, c].item()
