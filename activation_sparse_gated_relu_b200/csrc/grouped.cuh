@@ -393,10 +393,10 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         else mbar_arrive(&accfree[b]);
       }
     };
-    // columns c .. c + 31 of the tile, this thread's row m
+    // columns c .. c + 31 of the tile, this thread's row m; by whole warps
     auto store = [&](const float (&v)[32], int c) {
-      const int m = t.m0 + (int)rank * 128 + (warp & 3) * 32 + lane, n = t.cols - c;
-      if (m >= t.M) return;   // M is a multiple of 8: both lanes of a pair are in, or neither
+      const int m = t.m0 + (int)rank * 128 + (warp & 3) * 32 + lane;
+      const int n = m < t.M ? t.cols - c : 0;   // M is a multiple of 8: both lanes of a pair store, or neither
       if (args.out_f32) {
         float* o = reinterpret_cast<float*>(args.out) + (t.orow + c) * (size_t)t.M + m;
         if (n >= 32) {
@@ -413,11 +413,10 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         const int odd = lane & 1;
         const uint32_t sel = odd ? 0x3276u : 0x5410u;
         __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(args.out) + (t.orow + c + odd) * (size_t)t.M + (m - odd);
-        const unsigned mask = __activemask();
 #pragma unroll
         for (int i = 0; i < 32; i += 2, o += 2 * (size_t)t.M) {
           const uint32_t p = pack_bf16(v[i], v[i + 1]);
-          const uint32_t q = __shfl_xor_sync(mask, p, 1);
+          const uint32_t q = __shfl_xor_sync(0xFFFFFFFFu, p, 1);
           if (i + odd < n) *reinterpret_cast<uint32_t*>(o) = __byte_perm(p, q, sel);
         }
       }
