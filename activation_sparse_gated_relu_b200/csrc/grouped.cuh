@@ -355,7 +355,10 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
           const uint32_t d = tmem + (uint32_t)(b * BN);
           const int k1 = min(kc + args.kchunk, t.kbs);
           for (int kb = kc; kb < k1; ++kb) {
-            ok = mbar_wait(&full[s], ph, abort_flag, args.status);
+            // a block that the other CTA's threads cleared has to be seen as they left it
+            ok = CTAS == 2 && B_MN && kb == t.kbs - 1 && (t.ktail & 15)
+                     ? mbar_wait_cluster(&full[s], ph, abort_flag, args.status)
+                     : mbar_wait(&full[s], ph, abort_flag, args.status);
             if (!ok) break;
             tc_fence_after();
             const uint64_t ad = ad0 + (uint32_t)(s * (Cfg::STAGE / 16)), bd = bd0 + (uint32_t)(s * (Cfg::STAGE / 16));

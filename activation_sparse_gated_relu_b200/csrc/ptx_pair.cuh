@@ -49,6 +49,23 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
                                                uint32_t* status) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
 }
+// mbar_wait for a phase that threads of another CTA of the cluster arrived on
+// with mbar_release_cluster: what they wrote is seen.  The acquire is a second
+// look at the phase, which is complete by then and stays until the caller hands
+// its stage back; a wait that acquires at cluster scope at every try is slow.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                  uint32_t* status) {
+  if (!mbar_wait(bar, parity, abort_flag, status)) return false;
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 // Four bytes from global to shared memory, asynchronously; zero where `in` is false.
 __device__ __forceinline__ void copy4_async(void* dst, const void* src, bool in) {

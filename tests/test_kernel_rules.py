@@ -20,3 +20,16 @@ def test_no_warp_mask_from_the_lanes_that_happen_to_be_there():
     # may leave a lane's partner out
     for name in sorted(os.listdir(CSRC)):
         assert "__activemask" not in code(name), name
+
+
+def test_what_another_cta_cleared_is_acquired_at_cluster_scope():
+    # weight gradient: the clearing warp of each CTA of a pair releases its writes at cluster scope, so the one thread
+    # that issues the pair's MMAs has to acquire them at that scope, on the blocks that were cleared
+    ptx, kernel = code("ptx_pair.cuh"), code("grouped.cuh")
+    wait = ptx[ptx.index("mbar_wait_cluster("):]
+    assert "acquire.cluster" in wait[:wait.index("\n}")]
+    assert "arrive.release.cluster" in ptx[ptx.index("mbar_release_cluster("):].split("\n}")[0]
+    fix = kernel[kernel.index("warp == GT_FIX"):kernel.index("warp == GT_MMA) {")]
+    issue = kernel[kernel.index("warp == GT_MMA) {"):]
+    assert "mbar_release_cluster(" in fix
+    assert "mbar_wait_cluster(&full[s]" in issue
