@@ -503,6 +503,7 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   __syncwarp();
   tc_fence_before();
   if (BN == 32 && split > 1) {
+    spread_abort(abort_flag, split);
     cluster_sync();   // every CTA's sums are in its ring
     if (walk0 < n_tiles && warp < GT_EPI_WARPS) {
       // CTA `rank` adds up and stores every split-th column

@@ -66,6 +66,18 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
       : "memory");
   return ok != 0;
 }
+// Where a wait failed in this CTA, the other CTAs of its cluster learn of it.  By
+// every warp before the cluster barrier behind which they use each other's
+// results, so that behind it all of them find the flag set, or none.  (A wait
+// takes seconds to fail: every CTA has cleared its flag long before.)
+__device__ __forceinline__ void spread_abort(volatile int* abort_flag, int n_ctas) {
+  if (__any_sync(0xFFFFFFFFu, *abort_flag)) {
+    const uint32_t at = smem_u32(const_cast<const int*>(abort_flag));
+    for (int r = 0; r < n_ctas; ++r)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(at, (uint32_t)r)), "r"(1) : "memory");
+  }
+  __syncwarp();
+}
 
 // Four bytes from global to shared memory, asynchronously; zero where `in` is false.
 __device__ __forceinline__ void copy4_async(void* dst, const void* src, bool in) {

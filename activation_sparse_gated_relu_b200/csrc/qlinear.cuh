@@ -237,8 +237,9 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     for (int i = 0; i < BN / 2; ++i) sum[i] = 0;
     for (int i = wg; i < ns; i += 2) {
       const int s = i % STAGES, b = i % NBUF, kb = kb0 + i * KS;
-      // A failed wait is not acted on (nothing is stored then): leaving the
-      // loop from its middle would cost a select per sum.
+      // A failed wait is not acted on (nothing is stored then, by any CTA that
+      // shares the tile): leaving the loop from its middle would cost a select
+      // per sum.
       mbar_wait_warp(&sfull[s], (i / STAGES) & 1, abort_flag, a.status);
       mbar_wait_warp(&accfull[b], (i / NBUF) & 1, abort_flag, a.status);
       tc_fence_after();
@@ -295,6 +296,7 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   __syncwarp();
   tc_fence_before();
   if (a.split > 1) {
+    spread_abort(abort_flag, a.split);
     cluster_sync();   // every CTA's sums are in its ex
     // CTA `rank` adds up and stores every split-th column
     const int row = threadIdx.x & 127, m = m0 + row;
@@ -619,6 +621,7 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
   __syncwarp();
   tc_fence_before();
   if (BN == 128 && a.split > 1) {
+    spread_abort(abort_flag, a.split);
     cluster_sync();   // every CTA's sums are in its ring
     // CTA `rank` adds up and stores its part of every warp's 32 columns
     const int each = 32 / a.split, c0 = (warp >> 2) * 32 + rank * each;

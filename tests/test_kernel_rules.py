@@ -33,3 +33,21 @@ def test_what_another_cta_cleared_is_acquired_at_cluster_scope():
     issue = kernel[kernel.index("warp == GT_MMA) {"):]
     assert "mbar_release_cluster(" in fix
     assert "mbar_wait_cluster(&full[s]" in issue
+
+
+def test_a_failed_wait_keeps_every_cta_of_a_cluster_from_storing():
+    # where a cluster adds up its CTAs' parts, a CTA whose wait failed has none to give: all of them have to know before
+    # the barrier behind which the parts are read
+    sites = 0
+    for name in ("qlinear.cuh", "grouped.cuh"):
+        text = code(name)
+        for m in re.finditer(r"cluster_sums<", text):
+            before = text[:m.start()]
+            sync = before.rindex("cluster_sync();")
+            assert re.search(r"spread_abort\(abort_flag, \S+\);\s*$", before[:sync]), name
+            assert "!*abort_flag" in before[sync:], name
+            sites += 1
+    assert sites == 3
+    helper = code("ptx_pair.cuh")
+    helper = helper[helper.index("void spread_abort("):].split("\n}")[0]
+    assert "cluster_addr(" in helper and "st.shared::cluster" in helper
