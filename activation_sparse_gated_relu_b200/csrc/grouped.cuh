@@ -298,13 +298,6 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
         }
       }
     }
-    // After a timeout the CTA must not exit before its copies have landed.
-    // Their barriers may be the other CTA's or half-armed, so it waits the
-    // time that any copy takes many times over.
-    if (!ok) {
-      const uint64_t t0 = globaltimer();
-      while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
-    }
   } else if (warp == GT_FIX) {
     // --------------------------------------------------- weight gradient only
     // The last MMA of a group takes k up to the next multiple of 16: what lies
@@ -527,9 +520,16 @@ k_grouped(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtens
   }
   __syncthreads();
   // every MMA of this CTA (pair) is complete before TMEM is freed
-  if (warp == GT_MMA) mbar_wait_warp(mma_done, 0, abort_flag, args.status);
+  if (warp == GT_MMA) mbar_drain(mma_done, 0, args.status);
   __syncwarp();
-  if (CTAS == 2) cluster_sync();   // neither CTA leaves while the other may still signal or read it
+  if (CTAS == 2) {   // neither CTA leaves while the other may still signal or read it
+    spread_abort(abort_flag, 2);
+    cluster_sync();
+  }
+  if (*abort_flag) {
+    drain_copies();
+    if (CTAS == 2) cluster_sync();
+  }
   if (warp == GT_MMA) {
     tc_fence_after();
     pair_tmem_dealloc<CTAS>(tmem, NCOLS);

@@ -78,6 +78,24 @@ __device__ __forceinline__ void spread_abort(volatile int* abort_flag, int n_cta
   }
   __syncwarp();
 }
+// What a CTA that leaves, TMEM freed, must not have under way, also where a wait
+// has failed in any of its roles: MMAs (`bar` is committed to behind the last of
+// them; a bounded wait that goes on where another has failed) ...
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer() - t0 > SFFN_WAIT_LIMIT_NS) {
+      atomicOr(status, DEV_ERR_TIMEOUT);
+      break;
+    }
+  }
+}
+// ... and copies.  Their barriers may be another CTA's, or half-armed, so this
+// waits many times as long as any copy takes.
+__device__ __forceinline__ void drain_copies() {
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
+}
 
 // Four bytes from global to shared memory, asynchronously; zero where `in` is false.
 __device__ __forceinline__ void copy4_async(void* dst, const void* src, bool in) {

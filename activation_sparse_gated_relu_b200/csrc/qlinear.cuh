@@ -135,12 +135,10 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
   if (warp == QL_PRODUCER) {
     // --------------------------------------------------------- TMA producer
     // Weight rows past the end and columns of k past the end arrive as zeros.
-    bool ok = true;
     int s = 0;
     uint32_t ph = 1;
     for (int i = 0; i < ns; ++i) {
-      ok = mbar_wait_warp(&empty[s], ph, abort_flag, a.status);   // the first round passes
-      if (!ok) break;
+      if (!mbar_wait_warp(&empty[s], ph, abort_flag, a.status)) break;   // the first round passes
       if (elect_one()) {
         uint8_t* st = smem + (size_t)s * Cfg::STAGE;
         const int kb = kb0 + i * KS, nb = min(KS, kb1 - kb);
@@ -156,10 +154,6 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
         s = 0;
         ph ^= 1;
       }
-    }
-    if (!ok) {   // a CTA must not exit before its copies have landed: wait far longer than they take
-      const uint64_t t0 = globaltimer();
-      while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
     }
   } else if (warp == QL_SCALE) {
     // ----------------------------------------------------- scales, by stage
@@ -216,15 +210,7 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
       tc_commit(mma_done);
     }
     __syncwarp();
-    if (lane == 0) {   // every MMA is complete before TMEM is freed
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(mma_done, 0)) {
-        if (globaltimer() - t0 > SFFN_WAIT_LIMIT_NS) {
-          atomicOr(a.status, DEV_ERR_TIMEOUT);
-          break;
-        }
-      }
-    }
+    mbar_drain(mma_done, 0, a.status);   // every MMA is complete before TMEM is freed
   } else {
     // ------------------------------------------------------------- epilogue
     // Two warpgroups, every other stage each.
@@ -315,6 +301,7 @@ k_qlinear_cols(const __grid_constant__ CUtensorMap mW, const __grid_constant__ C
     cluster_sync();   // nobody leaves while its sums are read
   }
   __syncthreads();
+  if (*abort_flag) drain_copies();
   if (warp == QL_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, NCOLS);
@@ -450,10 +437,6 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
             ph ^= 1;
           }
         }
-      }
-      if (!ok) {   // a CTA must not exit before its copies have landed: wait far longer than they take
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 1000000ull) __nanosleep(1000);
       }
     } else if (warp == QR_SCALE) {
       // ------------------------------------------------------------- scales
@@ -639,8 +622,10 @@ k_qlinear_rows(const __grid_constant__ CUtensorMap mX, const __grid_constant__ C
     cluster_sync();   // nobody leaves while its sums are read
   }
   __syncthreads();
+  if (*abort_flag) drain_copies();
   if (warp == QR_MMA) {
-    mbar_wait_warp(mma_done, 0, abort_flag, a.status);   // every MMA is complete before TMEM is freed
+    mbar_drain(mma_done, 0, a.status);   // every MMA is complete before TMEM is freed
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -51,3 +51,23 @@ def test_a_failed_wait_keeps_every_cta_of_a_cluster_from_storing():
     helper = code("ptx_pair.cuh")
     helper = helper[helper.index("void spread_abort("):].split("\n}")[0]
     assert "cluster_addr(" in helper and "st.shared::cluster" in helper
+
+
+def test_nothing_is_under_way_when_a_cta_that_gave_up_leaves():
+    # a wait can fail in any role, after the producer has issued its last copy: what is under way then (copies into
+    # shared memory, MMAs that read it and write TMEM) has to be over before TMEM is freed and the CTA exits, whichever
+    # role gave up
+    for name, kernels in (("qlinear.cuh", 2), ("grouped.cuh", 1)):
+        text = code(name)
+        bodies = re.split(r"__global__", text)[1:]
+        assert len(bodies) == kernels
+        for body in bodies:
+            assert not re.search(r"mbar_wait\w*\(&?mma_done", body), name       # returns at once where a wait failed
+            assert "mbar_drain(mma_done" in body, name
+            last = body[body.rindex("__syncthreads();"):]                      # every role is over
+            assert re.search(r"if \(\*abort_flag\)\s*\{?\s*drain_copies\(\);", last), name
+            assert last.index("drain_copies();") < last.index("tmem_dealloc"), name
+    grouped = code("grouped.cuh")
+    end = grouped[grouped.rindex("__syncthreads();"):]                          # the pair's CTAs signal each other
+    assert re.search(r"spread_abort\(abort_flag, 2\);\s*cluster_sync\(\);.*drain_copies\(\);\s*if \(CTAS == 2\) cluster_sync\(\);",
+                     end, re.S)
