@@ -96,7 +96,8 @@ NormShape norm_shape(int d) {
 }
 
 // CTAs of the gradient: as many as the SMs' registers hold, at most four an SM,
-// since each leaves a partial sum of dw; with T and d alone, for the workspace.
+// since each leaves a partial sum of dw; with T and d alone, for the workspace
+// (148 SMs: on a device with another number the rounds are uneven, no more).
 int norm_bwd_ctas(const NormShape& s, int T, int per_sm) {
   const int most = s.nv == 4 ? 1 : std::min(4, 1024 / s.threads);
   return std::min(cdiv(T, s.rpc), 148 * std::min(most, per_sm));

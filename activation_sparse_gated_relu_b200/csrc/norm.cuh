@@ -18,8 +18,10 @@
 // 256; above that a CTA of as many warps as the row needs, so that neither the
 // second use of s nor the 8-bit scale reads global memory again.  Forward, 4096
 // rows of 2048, fp32 x, bf16 residual, sum and y (84 MB): 12.7 us, 6.6 TB/s; 6213
-// rows of 5400 51 us, 6.5 TB/s (62 with groups of a power of two).  Gradient, 8191
-// rows of 4096, all bf16 (268 MB): 49.1 us, 5.5 TB/s, and 3.7 for dw's partial
+// rows of 5400 51 us, 6.5 TB/s (62 with groups of a power of two).  To e4m3, all
+// bf16 before, 8192 rows of 4096 (236 MB) 50 us, 4.7 TB/s: a row is one chain of
+// load, sum, scale and store, and the codes leave 8 bytes a thread.  Gradient, 8191
+// rows of 4096, all bf16 (268 MB): 49.5 us, 5.4 TB/s, and 3.7 for dw's partial
 // sums.  Sums are fp32, in a fixed order.
 #pragma once
 
@@ -155,10 +157,13 @@ struct NormBwdArgs {
 // ahead, and reads them back itself, without any barrier, and again for their
 // second use.  That leaves 64 registers a thread enough up to 8192 columns, for
 // two CTAs of 512 threads an SM (four of 256).  Where the rows are too wide (d >
-// 8192 in fp32), STAGES is 0 and they are loaded as they are needed.  What is
-// left is bound by instruction issue, so the arithmetic runs on pairs of columns.
-// Measured at 8191 x 4096: rows loaded as they are needed, one column at a time
-// 70.5 us, so 49.1; at 4382 x 7656 the values in registers, one CTA, 82, so 63.
+// 8192 in fp32), STAGES is 0 and they are loaded as they are needed.  With four
+// stages, what is left is bound by instruction issue, so the arithmetic runs on
+// pairs of columns.  Measured at 8191 x 4096: rows loaded as they are needed, one
+// column at a time 70.5 us, so 49.5; at 4382 x 7656 the values in registers, one
+// CTA, 82, so 63.  With two stages (fp32 rows, or more than eight columns a thread)
+// only one row is on its way, and that bounds it: 8192 x 4096 fp32 110 us, 4.3 TB/s,
+// 6213 x 5400 bf16 65 us, 4.1 TB/s.
 template <bool SF32, bool DYF32, bool DS, int NV>
 struct NormBwdCfg {
   static constexpr int NS = SF32 ? 2 : 1, NY = DYF32 ? 2 : 1, ND = DS ? NS : 0;

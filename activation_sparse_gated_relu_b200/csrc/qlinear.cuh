@@ -9,8 +9,8 @@
 //
 // k_qlinear_cols: up to 32 tokens.  Weight rows are the MMA's 128 rows (TMEM
 // lanes), tokens its columns, so that a token costs little and W is read
-// once.  Bound by W's bytes: one token, d_in 4096, d_out 14336, 59 MB, 12.6 us of
-// which some 4 are launch and set-up.  An MMA of 128 x 16 x 32 takes 45 cycles
+// once.  Bound by W's bytes: one token, d_in 4096, d_out 14336, 59 MB, 12 to 13 us
+// of which some 4 are launch and set-up.  An MMA of 128 x 16 x 32 takes 45 cycles
 // however many of its rows are used, and looking at a barrier 50 to 100, so a
 // stage is two blocks with one barrier each way, and a narrow weight (few rows,
 // long k) is cut along k over the CTAs of a cluster, which add their sums up
@@ -18,13 +18,15 @@
 // d_out 4096, 18.5 us without and 14.4 with.
 //
 // k_qlinear_rows: more tokens.  Tokens are the MMA's rows, so that a token's
-// scale is one register per thread.  4096 tokens, d_in 4096, d_out 14336: 252 us,
+// scale is one register per thread.  4096 tokens, d_in 4096, d_out 14336: 253 us,
 // 1.9 PFLOP/s.  A block of 128 x 256 takes about 1000 cycles: 512 are MMAs, 768
 // the least that shared memory needs at 128 bytes a cycle (48 KB in by copies, 48
 // KB out to the MMAs), and the sums' way from TMEM takes 560.  CTA pairs, which
 // halve the weights' part, took 259 us (the second CTA's epilogue has to signal
 // the first); halves of 128 columns with barriers of their own 277 (the tokens
-// are read from shared memory twice).
+// are read from shared memory twice).  From 129 to some 1000 tokens whole rounds of
+// tiles bound it, with SMs idle in the last: 333 tokens, 4096 to 14336, 39 us, 14336
+// to 4096 42 us.
 #pragma once
 
 #include "ptx_pair.cuh"

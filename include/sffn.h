@@ -505,7 +505,9 @@ sffn_status sffn_moe_timing_end(sffn_moe_handle* h, int max_kernels, char (*name
  * NULL); weight [d] bf16 or fp32; y [T][d] bf16, fp32, or e4m3 codes with
  * scale [T][ceil(d/128)], one for each 128 columns (scale is NULL for the other
  * types).  eps finite, >= 0.  Sums of squares are fp32: they overflow (y = 0)
- * where |s| passes about 1e19 / sqrt(d).
+ * where |s| passes about 1e19 / sqrt(d), and with an eps of 0 they lose bits where
+ * a row stays below about 1e-19 (a row of zeros is 0 / 0 then).  y may replace an
+ * input of its own type, element by element.
  * Limits: d % 8 == 0, d <= 16384 (SFFN_ERR_UNSUPPORTED). */
 typedef struct sffn_rmsnorm_desc {
   int d;
@@ -578,11 +580,12 @@ sffn_status sffn_qlinear_destroy(sffn_qlinear_handle* h);
  *     forward          y[r]  = W[e] x[r]                 bf16 or fp32
  *     backward_input   dx[r] = W[e]^T dy[r]              bf16 or fp32
  *     backward_weight  dW[e] = sum_{r in e} dy[r] x[r]^T  bf16 or fp32
- * x [R][d_in], dy [R][d_out] bf16; sums fp32, rounded once.  Rows outside
+ * x [R][d_in], dy [R][d_out] bf16; sums fp32, rounded once (2^20 terms of one sign
+ * come out at most 2^-12 low for a bf16 output, 3e-6 for fp32).  Rows outside
  * every group are left as they were in y and dx; dW of an empty group is 0.
  * A row depends on no other row's values, not even NaN.  Offsets must not
- * decrease and lie in 0..R: the kernels clamp what does not (and start no group before all earlier
- * ones end) and record SFFN_ERR_DEVICE (sffn_grouped_read_status); the results
+ * decrease and lie in 0..R: the kernels clamp what does not (and start no group
+ * before all earlier ones end) and record SFFN_ERR_DEVICE (sffn_grouped_read_status); the results
  * of the groups concerned are then undefined.
  * Limits: n_experts <= 1024, d_in % 8 == 0, d_out % 8 == 0, both <= 2^20. */
 #define SFFN_GROUPED_MAX_EXPERTS 1024
